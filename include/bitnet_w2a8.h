@@ -361,6 +361,138 @@ int bitnet_pack_b3(const uint8_t* packed, int64_t N, int64_t K, uint8_t* b3, voi
 int bitnet_quant_gemv_b3(const uint16_t* x, const uint8_t* b3, const float* w_scale, int64_t M,
                          int64_t N, int64_t K, void* out, int out_dtype, void* stream);
 
+/* ==================================================================================
+ * The training side of a BitLinear layer: the norm in front of it, 8-bit checkpoints of
+ * activations, SwiGLU, and the gradients of the product.  "BitNet 深度实战" §2.3 trains the
+ * layer with straight-through quantizers: the forward multiplies the rounded activations
+ * and weights, the backward passes gradients through both roundings unchanged.
+ *
+ * Activations and their gradients are bf16 (uint16 bit patterns); norm weights, statistics
+ * and scales are fp32.  All sums are accumulated in fp32, in an order that depends on the
+ * sizes only: a call gives the same bits every time.  Output buffers must not overlap one
+ * another or any input.  Where the M rows of a sum are empty the sum is zero: M == 0 clears
+ * dweight, dbias and dw instead of leaving them.  NULL is accepted where "optional" is said.
+ * ================================================================================== */
+
+/* Scale of a token's int8 codes. */
+typedef enum {
+    BITNET_SCALE_ABSMAX = 0, /* a = 127 / max(amax, 1e-5), as bitnet_quant_act            */
+    BITNET_SCALE_POW2 = 1    /* the largest power of two not above that                   */
+} bitnet_scale_kind;
+
+/*
+ * bitnet_quant_act_pow2 -- an activation's 8-bit checkpoint: bitnet_quant_act with
+ *   a_scale[m] = 2^floor(log2(127 / max(max_k |x[m,k]|, 1e-5))).
+ * x * a is exact, so xq is the round-half-even of the exact value, and xq / a is exact in
+ * bf16: bitnet_grad_weight on such codes has no rounding before its fp32 sum.  The product
+ * entry points take these codes like any others.
+ */
+int bitnet_quant_act_pow2(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, float* a_scale,
+                          void* stream);
+
+/*
+ * bitnet_dequant_act -- the values that codes stand for, x[m,k] = bf16(xq[m,k] / a_scale[m])
+ * (one fp32 division and one rounding; exact for power-of-two scales).
+ */
+int bitnet_dequant_act(const int8_t* xq, const float* a_scale, int64_t M, int64_t K, uint16_t* x,
+                       void* stream);
+
+/*
+ * bitnet_layernorm -- layer norm over K, with the int8 codes of its output fused in.
+ *   mean[m] = mean_k x, rstd[m] = 1 / sqrt(mean_k (x - mean)^2 + eps),
+ *   y = (x - mean) * rstd * weight + bias in fp32, rounded to bf16.
+ *   weight, bias : float (K), optional (1 and 0).   eps > 0, finite.
+ *   y            : bf16 (M, K), optional.
+ *   xq, a_scale  : int8 (M, K) and float (M), both or neither: bit-identical to
+ *                  bitnet_quant_act (scale = BITNET_SCALE_ABSMAX) or bitnet_quant_act_pow2
+ *                  (BITNET_SCALE_POW2) of the bf16 y.  y or xq is needed.
+ *   mean, rstd   : float (M) each, optional; the backward takes them.
+ */
+int bitnet_layernorm(const uint16_t* x, const float* weight, const float* bias, float eps,
+                     int64_t M, int64_t K, uint16_t* y, int8_t* xq, float* a_scale, int scale,
+                     float* mean, float* rstd, void* stream);
+
+/*
+ * bitnet_layernorm_backward -- with xh = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - mean_k g - xh * mean_k (g * xh)), rounded to bf16;
+ *   dweight[k] = sum_m dy * xh,  dbias[k] = sum_m dy   (fp32, each optional).
+ *   x, x_scale : bf16 (M, K) with x_scale NULL, or the checkpoint: int8 (M, K) codes with
+ *                their float (M) scales, x ~ xq / x_scale.
+ *   weight     : float (K), optional (1).   mean, rstd : of the forward.
+ *   workspace  : with dweight or dbias, bitnet_layernorm_backward_workspace_size(M, K) bytes
+ *                of scratch (else BITNET_ERR_WORKSPACE); calls that share one must be ordered.
+ */
+size_t bitnet_layernorm_backward_workspace_size(int64_t M, int64_t K);
+int bitnet_layernorm_backward(const uint16_t* dy, const void* x, const float* x_scale,
+                              const float* weight, const float* mean, const float* rstd, int64_t M,
+                              int64_t K, uint16_t* dx, float* dweight, float* dbias,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * bitnet_swiglu -- h = silu(g) * u for any M (the products of gate and up, bf16), with what
+ * training keeps: the codes of h for the down projection and for its weight gradient, and
+ * 8-bit checkpoints of g and u.  N % 4 == 0, N <= BITNET_MAX_K.
+ *   h            : bf16 (M, N), optional.
+ *   hq, h_scale  : int8 (M, N) and float (M), both or neither: bit-identical to
+ *                  bitnet_quant_act or _pow2 (by `scale`) of the bf16 h.  h or hq is needed.
+ *   gq, g_scale, uq, u_scale : all or none: bitnet_quant_act_pow2 of g and of u.
+ */
+int bitnet_swiglu(const uint16_t* g, const uint16_t* u, int64_t M, int64_t N, uint16_t* h,
+                  int8_t* hq, float* h_scale, int scale, int8_t* gq, float* g_scale, int8_t* uq,
+                  float* u_scale, void* stream);
+
+/*
+ * bitnet_swiglu_backward -- with s = 1 / (1 + exp(-g)):
+ *   dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s   (fp32, rounded to bf16).
+ *   g, g_scale, u, u_scale : bf16 (M, N) with both scales NULL, or checkpoints: int8 codes
+ *                            with their float (M) scales.
+ */
+int bitnet_swiglu_backward(const uint16_t* dh, const void* g, const float* g_scale, const void* u,
+                           const float* u_scale, int64_t M, int64_t N, uint16_t* dg, uint16_t* du,
+                           void* stream);
+
+/*
+ * bitnet_grad_input -- gradient of up to BITNET_MAX_GROUPS products with respect to the
+ * activations they share (one product; gate and up; q, k and v):
+ *   dx[m,k] = sum_g sum_n dy_g[m,n] * w_scale_g[n] * w_g[n,k].
+ *   dy, packed, w_scale, N : HOST arrays of `groups` entries, read during the call only: bf16
+ *                (M, N[g]), uint8 (N[g], K/4), float (N[g]) device pointers.  N[g] == 0 adds
+ *                nothing; N[g] <= BITNET_MAX_K.  An unused code 0b11 counts as weight 0.
+ *   dx         : bf16 (M, K).  Each dy * w_scale is rounded to bf16 once, products with w and
+ *                their sum are fp32, and the sum over all groups is rounded once.
+ *   workspace  : optional scratch: with bitnet_grad_input_workspace_size bytes the sum is split
+ *                over blocks where the output is small; with less the call runs unsplit (sums
+ *                in another order).  Calls that share one must be ordered.
+ */
+size_t bitnet_grad_input_workspace_size(int64_t M, int64_t K, int64_t groups, const int64_t* N);
+int bitnet_grad_input(int64_t M, int64_t K, int64_t groups, const uint16_t* const* dy,
+                      const uint8_t* const* packed, const float* const* w_scale, const int64_t* N,
+                      uint16_t* dx, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * bitnet_grad_weight -- gradient with respect to the latent weights, from the forward's codes:
+ *   dw[n,k] = sum_m dy[m,n] * xq[m,k] / a_scale[m].
+ *   dy         : bf16 (M, N), N <= BITNET_MAX_K.
+ *   xq, a_scale: int8 (M, K) and float (M).  Each xq / a is rounded to bf16 once; it is exact
+ *                for power-of-two scales (bitnet_quant_act_pow2), and then only the fp32 sum
+ *                and the output round.
+ *   dw         : (N, K), BITNET_OUT_F32 or BITNET_OUT_BF16.
+ *   workspace  : as in bitnet_grad_input.
+ */
+size_t bitnet_grad_weight_workspace_size(int64_t M, int64_t N, int64_t K);
+int bitnet_grad_weight(const uint16_t* dy, const int8_t* xq, const float* a_scale, int64_t M,
+                       int64_t N, int64_t K, void* dw, int out_dtype, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * bitnet_grad_plan -- the plan bitnet_grad_input (weight == 0) or bitnet_grad_weight
+ * (weight != 0, groups == 1) takes with its workspace.  Host-only: launches nothing.
+ *   plan : HOST int32[4] output = tile rows, tile columns, groups of waves per tile that
+ *          share the sum, slices of the sum over blocks (1: unsplit).
+ */
+int bitnet_grad_plan(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N,
+                     int32_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -79,6 +79,19 @@ def lib():
             "bitnet_repack_codes": ([p, i64, i64, i32, i32, p, p, p], i32),
             "bitnet_pack_b3": ([p, i64, i64, p, p], i32),
             "bitnet_quant_gemv_b3": ([p, p, p, i64, i64, i64, p, i32, p], i32),
+            "bitnet_quant_act_pow2": ([p, i64, i64, p, p, p], i32),
+            "bitnet_dequant_act": ([p, p, i64, i64, p, p], i32),
+            "bitnet_layernorm": ([p, p, p, ctypes.c_float, i64, i64, p, p, p, i32, p, p, p], i32),
+            "bitnet_layernorm_backward_workspace_size": ([i64, i64], ctypes.c_size_t),
+            "bitnet_layernorm_backward": ([p, p, p, p, p, p, i64, i64, p, p, p, p, ctypes.c_size_t,
+                                           p], i32),
+            "bitnet_swiglu": ([p, p, i64, i64, p, p, p, i32, p, p, p, p, p], i32),
+            "bitnet_swiglu_backward": ([p, p, p, p, p, i64, i64, p, p, p], i32),
+            "bitnet_grad_input_workspace_size": ([i64, i64, i64, p], ctypes.c_size_t),
+            "bitnet_grad_input": ([i64, i64, i64, p, p, p, p, p, p, ctypes.c_size_t, p], i32),
+            "bitnet_grad_plan": ([i32, i64, i64, i64, p, p], i32),
+            "bitnet_grad_weight_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
+            "bitnet_grad_weight": ([p, p, p, i64, i64, i64, p, i32, p, ctypes.c_size_t, p], i32),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -470,3 +483,265 @@ def bitlinear(x, packed, w_scale, out_dtype="f32"):
         return quant_gemv(x, packed, w_scale, out_dtype)
     xq, a_scale = quant_act(x)
     return gemm(xq, a_scale, packed, w_scale, out_dtype)
+
+
+# ------------------------------------------------------------ the training side of a layer
+
+SCALE_ABSMAX, SCALE_POW2 = 0, 1
+_SCALE_NAMES = {"absmax": SCALE_ABSMAX, "pow2": SCALE_POW2}
+
+
+def _scale_code(scale) -> int:
+    return _SCALE_NAMES[scale] if isinstance(scale, str) else int(scale)
+
+
+def _arg(t, dtype, name, shape, device):
+    """_tensor of an argument that has to lie on `device`; None (optional) stays None."""
+    if t is None:
+        return None
+    ptr = _tensor(t, dtype, name, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return ptr
+
+
+def _run(name, device, *args):
+    """Call an entry point with `device` current and its current stream as the last argument."""
+    fn = getattr(lib(), name)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    _check(status, name)
+
+
+def _rows(t, name):
+    """(M, K) of a device matrix."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor (the library has no CPU path)")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _scratch(need, workspace, device):
+    """(pointer, bytes) of a workspace: the caller's, or one of `need` bytes."""
+    if workspace is False:
+        return None, 0, None
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+    return _arg(workspace, torch.uint8, "workspace", None, device), workspace.numel(), workspace
+
+
+def quant_act_pow2(x, xq=None, a_scale=None):
+    """8-bit checkpoint of bf16 (M, K): (xq int8 (M, K), a_scale fp32 (M,)), a_scale the largest
+    power of two that keeps |x * a_scale| <= 127; xq / a_scale is exact in bf16."""
+    M, K = _rows(x, "x")
+    d = x.device
+    if xq is None:
+        xq = torch.empty((M, K), dtype=torch.int8, device=d)
+    if a_scale is None:
+        a_scale = torch.empty((M,), dtype=torch.float32, device=d)
+    _run("bitnet_quant_act_pow2", d, _arg(x, torch.bfloat16, "x", (M, K), d), M, K,
+         _arg(xq, torch.int8, "xq", (M, K), d), _arg(a_scale, torch.float32, "a_scale", (M,), d))
+    return xq, a_scale
+
+
+def dequant_act(xq, a_scale, out=None):
+    """The values int8 codes stand for: bf16(xq / a_scale), (M, K)."""
+    M, K = _rows(xq, "xq")
+    d = xq.device
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=d)
+    _run("bitnet_dequant_act", d, _arg(xq, torch.int8, "xq", (M, K), d),
+         _arg(a_scale, torch.float32, "a_scale", (M,), d), M, K,
+         _arg(out, torch.bfloat16, "out", (M, K), d))
+    return out
+
+
+def _layernorm(x, weight, bias, eps, want_y, scale, return_stats, out=None):
+    M, K = _rows(x, "x")
+    d = x.device
+    y, xq, a_scale, mean, rstd = out, None, None, None, None
+    if want_y and y is None:
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=d)
+    if scale is not None:
+        xq = torch.empty((M, K), dtype=torch.int8, device=d)
+        a_scale = torch.empty((M,), dtype=torch.float32, device=d)
+    if return_stats:
+        mean = torch.empty((M,), dtype=torch.float32, device=d)
+        rstd = torch.empty((M,), dtype=torch.float32, device=d)
+    ptr = lambda t: None if t is None else t.data_ptr()  # our own allocations
+    _run("bitnet_layernorm", d, _arg(x, torch.bfloat16, "x", (M, K), d),
+         _arg(weight, torch.float32, "weight", (K,), d), _arg(bias, torch.float32, "bias", (K,), d),
+         float(eps), M, K, _arg(y, torch.bfloat16, "out", (M, K), d), ptr(xq), ptr(a_scale),
+         0 if scale is None else scale, ptr(mean), ptr(rstd))
+    return y, xq, a_scale, mean, rstd
+
+
+def layernorm(x, weight=None, bias=None, eps=1e-5, return_stats=False, out=None):
+    """Layer norm of bf16 (M, K) over K with fp32 weight and bias (None: 1 and 0) -> bf16 y, or
+    (y, mean, rstd) with the fp32 (M,) statistics that layernorm_backward takes."""
+    y, _, _, mean, rstd = _layernorm(x, weight, bias, eps, True, None, return_stats, out)
+    return (y, mean, rstd) if return_stats else y
+
+
+def layernorm_quant(x, weight=None, bias=None, eps=1e-5, scale="absmax", return_y=False,
+                    return_stats=False):
+    """Layer norm with the int8 codes of its output in one launch: what quant_act (scale
+    "absmax") or quant_act_pow2 ("pow2") gives for layernorm's y.  Returns (xq, a_scale), then y
+    with return_y, then mean and rstd with return_stats."""
+    y, xq, a, mean, rstd = _layernorm(x, weight, bias, eps, return_y, _scale_code(scale),
+                                      return_stats)
+    return (xq, a) + ((y,) if return_y else ()) + ((mean, rstd) if return_stats else ())
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, x_scale=None, need_sums=True, workspace=None):
+    """(dx bf16 (M, K), dweight fp32 (K,), dbias fp32 (K,)) of layernorm; dweight and dbias are
+    None with need_sums=False.  x: the bf16 input, or its 8-bit checkpoint (int8 codes) with
+    x_scale.  workspace: uint8 scratch of bitnet_layernorm_backward_workspace_size bytes
+    (allocated by default)."""
+    M, K = _rows(dy, "dy")
+    d = dy.device
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device=d)
+    dweight = dbias = None
+    ws_ptr, ws_bytes, ws = None, 0, None
+    if need_sums:
+        dweight = torch.empty((K,), dtype=torch.float32, device=d)
+        dbias = torch.empty((K,), dtype=torch.float32, device=d)
+        need = int(lib().bitnet_layernorm_backward_workspace_size(M, K))
+        ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
+    _run("bitnet_layernorm_backward", d, _arg(dy, torch.bfloat16, "dy", (M, K), d),
+         _arg(x, torch.bfloat16 if x_scale is None else torch.int8, "x", (M, K), d),
+         _arg(x_scale, torch.float32, "x_scale", (M,), d),
+         _arg(weight, torch.float32, "weight", (K,), d), _arg(mean, torch.float32, "mean", (M,), d),
+         _arg(rstd, torch.float32, "rstd", (M,), d), M, K, dx.data_ptr(),
+         None if dweight is None else dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
+         ws_ptr, ws_bytes)
+    return dx, dweight, dbias
+
+
+def _swiglu(g, u, want_h, scale, checkpoint, out=None):
+    M, N = _rows(g, "g")
+    d = g.device
+    i8 = lambda: torch.empty((M, N), dtype=torch.int8, device=d)
+    f32 = lambda: torch.empty((M,), dtype=torch.float32, device=d)
+    ptr = lambda t: None if t is None else t.data_ptr()  # our own allocations
+    h, hq, hs, ckpt = out, None, None, None
+    if want_h and h is None:
+        h = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+    if scale is not None:
+        hq, hs = i8(), f32()
+    if checkpoint:
+        ckpt = (i8(), i8(), f32(), f32())
+    gq, uq, gs, us = ckpt if ckpt else (None,) * 4
+    _run("bitnet_swiglu", d, _arg(g, torch.bfloat16, "g", (M, N), d),
+         _arg(u, torch.bfloat16, "u", (M, N), d), M, N, _arg(h, torch.bfloat16, "out", (M, N), d),
+         ptr(hq), ptr(hs), 0 if scale is None else scale, ptr(gq), ptr(gs), ptr(uq), ptr(us))
+    return h, hq, hs, ckpt
+
+
+def swiglu(g, u, checkpoint=False, out=None):
+    """silu(g) * u of bf16 (M, N), any M -> bf16 h; with checkpoint, (h, (gq, uq, g_scale,
+    u_scale)): the 8-bit checkpoints that swiglu_backward(dh, *ckpt) takes."""
+    h, _, _, ckpt = _swiglu(g, u, True, None, checkpoint, out)
+    return (h, ckpt) if checkpoint else h
+
+
+def swiglu_quant(g, u, scale="absmax", return_h=False, checkpoint=False):
+    """silu(g) * u as int8 codes for the down projection, in one launch: what quant_act or
+    quant_act_pow2 (scale "pow2") gives for swiglu's h.  Returns (hq, h_scale), then h with
+    return_h, then the checkpoints of swiglu with checkpoint."""
+    h, hq, hs, ckpt = _swiglu(g, u, return_h, _scale_code(scale), checkpoint)
+    return (hq, hs) + ((h,) if return_h else ()) + ((ckpt,) if checkpoint else ())
+
+
+def swiglu_backward(dh, g, u, g_scale=None, u_scale=None):
+    """(dg, du) bf16 of swiglu from bf16 g and u, or from their checkpoints (int8 codes with
+    g_scale and u_scale)."""
+    M, N = _rows(dh, "dh")
+    d = dh.device
+    if (g_scale is None) != (u_scale is None):
+        raise ValueError("g_scale and u_scale go together")
+    dt = torch.bfloat16 if g_scale is None else torch.int8
+    dg = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+    du = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+    _run("bitnet_swiglu_backward", d, _arg(dh, torch.bfloat16, "dh", (M, N), d),
+         _arg(g, dt, "g", (M, N), d), _arg(g_scale, torch.float32, "g_scale", (M,), d),
+         _arg(u, dt, "u", (M, N), d), _arg(u_scale, torch.float32, "u_scale", (M,), d), M, N,
+         dg.data_ptr(), du.data_ptr())
+    return dg, du
+
+
+def grad_input_grouped(dy, packed, w_scale, out=None, workspace=None):
+    """Gradient of up to MAX_GROUPS products with respect to the input they share, summed:
+    dx = sum_g dy_g (w_scale_g * w_g), bf16 (M, K).
+
+    dy / packed / w_scale: sequences of bf16 (M, N_g), uint8 (N_g, K/4), fp32 (N_g,).
+    workspace: as in gemm (allocated by default; False: none)."""
+    G = len(dy)
+    if G == 0 or len(packed) != G or len(w_scale) != G:
+        raise ValueError("dy, packed and w_scale must have the same length, at least 1")
+    M = _rows(dy[0], "dy[0]")[0]
+    K = 4 * _rows(packed[0], "packed[0]")[1]
+    d = dy[0].device
+    Ns = [int(_rows(t, f"packed[{g}]")[0]) for g, t in enumerate(packed)]
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=d)
+    ptrs = ctypes.c_void_p * G
+    DY = ptrs(*[_arg(t, torch.bfloat16, f"dy[{g}]", (M, Ns[g]), d) for g, t in enumerate(dy)])
+    P = ptrs(*[_arg(t, torch.uint8, f"packed[{g}]", (Ns[g], K // 4), d) for g, t in enumerate(packed)])
+    S = ptrs(*[_arg(t, torch.float32, f"w_scale[{g}]", (Ns[g],), d) for g, t in enumerate(w_scale)])
+    NN = (ctypes.c_int64 * G)(*Ns)
+    need = int(lib().bitnet_grad_input_workspace_size(M, K, G, NN)) if workspace is None else 0
+    ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
+    _run("bitnet_grad_input", d, M, K, G, DY, P, S, NN, _arg(out, torch.bfloat16, "out", (M, K), d),
+         ws_ptr, ws_bytes)
+    return out
+
+
+def grad_input(dy, packed, w_scale, out=None, workspace=None):
+    """Gradient of a product with respect to its activations (straight-through quantizer):
+    bf16 (M, K) from dy bf16 (M, N) and the packed ternary weights."""
+    return grad_input_grouped([dy], [packed], [w_scale], out, workspace)
+
+
+def grad_weight(dy, xq, a_scale, out_dtype="f32", out=None, workspace=None):
+    """Gradient of a product with respect to its latent weights, (N, K): dy^T (xq / a_scale)
+    from dy bf16 (M, N) and the forward's int8 codes; exact products for quant_act_pow2's."""
+    M, N = _rows(dy, "dy")
+    K = _rows(xq, "xq")[1]
+    d = dy.device
+    code = _out_code(out_dtype)
+    if code == OUT_I32:
+        raise ValueError("the weight gradient is fp32 or bf16")
+    out = _alloc_out(out, N, K, code, d)
+    need = int(lib().bitnet_grad_weight_workspace_size(M, N, K)) if workspace is None else 0
+    ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
+    _run("bitnet_grad_weight", d, _arg(dy, torch.bfloat16, "dy", (M, N), d),
+         _arg(xq, torch.int8, "xq", (M, K), d), _arg(a_scale, torch.float32, "a_scale", (M,), d),
+         M, N, K, _arg(out, _OUT_TORCH[code], "out", (N, K), d), code, ws_ptr, ws_bytes)
+    return out
+
+
+def grad_plan(M, K, Ns, weight=False):
+    """Plan (tile rows, tile columns, wave groups, slices) of grad_input_grouped over matrices
+    of Ns rows, or with weight=True of grad_weight for one; host-only."""
+    G = len(Ns)
+    NN = (ctypes.c_int64 * max(G, 1))(*[int(n) for n in Ns])
+    out = (ctypes.c_int32 * 4)()
+    _check(lib().bitnet_grad_plan(int(weight), int(M), int(K), G, NN, out), "bitnet_grad_plan")
+    return tuple(int(v) for v in out)
+
+
+def bitlinear_backward(dy, xq, a_scale, packed, w_scale, dw_dtype="f32"):
+    """Both gradients of one BitLinear forward on the codes xq, a_scale: (dx bf16 (M, K),
+    dw (N, K) of dw_dtype)."""
+    return (grad_input(dy, packed, w_scale),
+            grad_weight(dy, xq, a_scale, out_dtype=dw_dtype))

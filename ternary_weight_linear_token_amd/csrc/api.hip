@@ -4,6 +4,7 @@
 // returns a bitnet_status code; nothing throws across the ABI.  Work is enqueued on the
 // caller's stream; nothing here synchronizes or allocates.
 #include <atomic>
+#include <cfloat>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -62,6 +63,20 @@ int check_shape(int64_t M, int64_t N, int64_t K) {
 
 bool valid_dtype(int dt) {
     return dt == BITNET_OUT_F32 || dt == BITNET_OUT_BF16 || dt == BITNET_OUT_I32;
+}
+
+bool valid_scale(int s) { return s == BITNET_SCALE_ABSMAX || s == BITNET_SCALE_POW2; }
+
+// Shapes of a grouped input gradient: N[g] is the length summed over, at most BITNET_MAX_K
+// (the kernels' 32-bit offsets into a block of rows).
+int check_grad_groups(int64_t M, int64_t K, int64_t groups, const int64_t* N) {
+    if (groups < 1 || groups > BITNET_MAX_GROUPS || !N) return BITNET_ERR_INVALID_ARG;
+    for (int64_t g = 0; g < groups; ++g) {
+        const int st = check_shape(M, N[g], K);
+        if (st) return st;
+        if (N[g] > BITNET_MAX_K) return BITNET_ERR_INVALID_ARG;
+    }
+    return BITNET_OK;
 }
 
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
@@ -456,6 +471,170 @@ int bitnet_quant_gemv_swiglu(const uint16_t* x, const uint8_t* packed_gate,
     return record_hip(bitnet::launch_skinny_swiglu(x, packed_gate, w_scale_gate, packed_up,
                                                    w_scale_up, M, N, K, h, out_dtype, xq_out,
                                                    a_scale_out, as_stream(stream)));
+}
+
+// ---- the training side of a layer ----
+
+int bitnet_quant_act_pow2(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, float* a_scale,
+                          void* stream) {
+    int st = check_shape(M, 0, K);
+    if (st) return st;
+    if (M == 0) return BITNET_OK;
+    if (!x || !xq || !a_scale) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(xq) || !aligned16(a_scale)) return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_quant_act_pow2(x, M, K, xq, a_scale, as_stream(stream)));
+}
+
+int bitnet_dequant_act(const int8_t* xq, const float* a_scale, int64_t M, int64_t K, uint16_t* x,
+                       void* stream) {
+    int st = check_shape(M, 0, K);
+    if (st) return st;
+    if (M == 0) return BITNET_OK;
+    if (!x || !xq || !a_scale) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(xq) || !aligned16(a_scale)) return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_dequant_act(xq, a_scale, M, K, x, as_stream(stream)));
+}
+
+int bitnet_layernorm(const uint16_t* x, const float* weight, const float* bias, float eps,
+                     int64_t M, int64_t K, uint16_t* y, int8_t* xq, float* a_scale, int scale,
+                     float* mean, float* rstd, void* stream) {
+    if (!valid_scale(scale)) return BITNET_ERR_INVALID_ARG;
+    if (!(eps > 0.0f) || eps > FLT_MAX) return BITNET_ERR_INVALID_ARG;
+    int st = check_shape(M, 0, K);
+    if (st) return st;
+    if (M == 0) return BITNET_OK;
+    if (!x || (!y && !xq) || (xq != nullptr) != (a_scale != nullptr)) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(weight) || !aligned16(bias) || !aligned16(y) || !aligned16(xq) ||
+        !aligned16(a_scale) || !aligned16(mean) || !aligned16(rstd))
+        return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_layernorm(x, weight, bias, eps, M, K, y, xq, a_scale,
+                                               scale == BITNET_SCALE_POW2, mean, rstd,
+                                               as_stream(stream)));
+}
+
+size_t bitnet_layernorm_backward_workspace_size(int64_t M, int64_t K) {
+    if (check_shape(M, 0, K) != BITNET_OK || M == 0) return 0;
+    return bitnet::layernorm_back_workspace_size(M, K);
+}
+
+int bitnet_layernorm_backward(const uint16_t* dy, const void* x, const float* x_scale,
+                              const float* weight, const float* mean, const float* rstd, int64_t M,
+                              int64_t K, uint16_t* dx, float* dweight, float* dbias,
+                              void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_shape(M, 0, K);
+    if (st) return st;
+    if (M == 0 && !dweight && !dbias) return BITNET_OK;
+    if (M > 0 && (!dy || !x || !mean || !rstd || !dx)) return BITNET_ERR_INVALID_ARG;
+    if (ws_bytes > 0 && !workspace) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(x_scale) || !aligned16(weight) ||
+        !aligned16(mean) || !aligned16(rstd) || !aligned16(dx) || !aligned16(dweight) ||
+        !aligned16(dbias) || !aligned16(workspace))
+        return BITNET_ERR_UNALIGNED;
+    if (M > 0 && (dweight || dbias) && ws_bytes < bitnet::layernorm_back_workspace_size(M, K))
+        return BITNET_ERR_WORKSPACE;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_layernorm_back(dy, x, x_scale, weight, mean, rstd, M, K, dx,
+                                                    dweight, dbias, workspace, as_stream(stream)));
+}
+
+int bitnet_swiglu(const uint16_t* g, const uint16_t* u, int64_t M, int64_t N, uint16_t* h,
+                  int8_t* hq, float* h_scale, int scale, int8_t* gq, float* g_scale, int8_t* uq,
+                  float* u_scale, void* stream) {
+    if (!valid_scale(scale)) return BITNET_ERR_INVALID_ARG;
+    int st = check_shape(M, 0, N);  // N is the K of the product that reads h
+    if (st) return st;
+    if (M == 0) return BITNET_OK;
+    if (!g || !u || (!h && !hq) || (hq != nullptr) != (h_scale != nullptr))
+        return BITNET_ERR_INVALID_ARG;
+    const int kept = (gq != nullptr) + (g_scale != nullptr) + (uq != nullptr) + (u_scale != nullptr);
+    if (kept != 0 && kept != 4) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(g) || !aligned16(u) || !aligned16(h) || !aligned16(hq) || !aligned16(h_scale) ||
+        !aligned16(gq) || !aligned16(g_scale) || !aligned16(uq) || !aligned16(u_scale))
+        return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_swiglu(g, u, M, N, h, hq, h_scale, scale == BITNET_SCALE_POW2,
+                                            gq, g_scale, uq, u_scale, as_stream(stream)));
+}
+
+int bitnet_swiglu_backward(const uint16_t* dh, const void* g, const float* g_scale, const void* u,
+                           const float* u_scale, int64_t M, int64_t N, uint16_t* dg, uint16_t* du,
+                           void* stream) {
+    int st = check_shape(M, 0, N);
+    if (st) return st;
+    if (M == 0) return BITNET_OK;
+    if (!dh || !g || !u || !dg || !du || (g_scale != nullptr) != (u_scale != nullptr))
+        return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(dh) || !aligned16(g) || !aligned16(g_scale) || !aligned16(u) ||
+        !aligned16(u_scale) || !aligned16(dg) || !aligned16(du))
+        return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_swiglu_back(dh, g, g_scale, u, u_scale, M, N, dg, du,
+                                                 as_stream(stream)));
+}
+
+size_t bitnet_grad_input_workspace_size(int64_t M, int64_t K, int64_t groups, const int64_t* N) {
+    if (check_grad_groups(M, K, groups, N) != BITNET_OK || M == 0) return 0;
+    return bitnet::grad_input_workspace_size(M, K, (int)groups, N);
+}
+
+int bitnet_grad_input(int64_t M, int64_t K, int64_t groups, const uint16_t* const* dy,
+                      const uint8_t* const* packed, const float* const* w_scale, const int64_t* N,
+                      uint16_t* dx, void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_grad_groups(M, K, groups, N);
+    if (st) return st;
+    if (!dy || !packed || !w_scale) return BITNET_ERR_INVALID_ARG;
+    if (M == 0) return BITNET_OK;
+    if (!dx || (ws_bytes > 0 && !workspace)) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(dx) || !aligned16(workspace)) return BITNET_ERR_UNALIGNED;
+    for (int64_t g = 0; g < groups; ++g) {
+        if (N[g] == 0) continue;
+        if (!dy[g] || !packed[g] || !w_scale[g]) return BITNET_ERR_INVALID_ARG;
+        if (!aligned16(dy[g]) || !aligned16(packed[g]) || !aligned16(w_scale[g]))
+            return BITNET_ERR_UNALIGNED;
+    }
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_grad_input(dy, packed, w_scale, N, (int)groups, M, K, dx,
+                                                workspace, ws_bytes, as_stream(stream)));
+}
+
+int bitnet_grad_plan(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N,
+                     int32_t* plan) {
+    const int st = check_grad_groups(M, K, groups, N);
+    if (st) return st;
+    if (!plan || M < 1 || (weight && (groups != 1 || N[0] < 1))) return BITNET_ERR_INVALID_ARG;
+    int p[4];
+    if (weight)
+        bitnet::grad_plan(0, N[0], K, &M, 1, p);
+    else
+        bitnet::grad_plan(1, M, K, N, (int)groups, p);
+    for (int i = 0; i < 4; ++i) plan[i] = p[i];
+    return BITNET_OK;
+}
+
+size_t bitnet_grad_weight_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (check_shape(M, N, K) != BITNET_OK || M == 0 || N == 0 || N > BITNET_MAX_K) return 0;
+    return bitnet::grad_weight_workspace_size(M, N, K);
+}
+
+int bitnet_grad_weight(const uint16_t* dy, const int8_t* xq, const float* a_scale, int64_t M,
+                       int64_t N, int64_t K, void* dw, int out_dtype, void* workspace,
+                       size_t ws_bytes, void* stream) {
+    if (out_dtype != BITNET_OUT_F32 && out_dtype != BITNET_OUT_BF16) return BITNET_ERR_INVALID_ARG;
+    int st = check_shape(M, N, K);
+    if (st) return st;
+    if (N > BITNET_MAX_K) return BITNET_ERR_INVALID_ARG;
+    if (N == 0) return BITNET_OK;
+    if (!dw || (ws_bytes > 0 && !workspace)) return BITNET_ERR_INVALID_ARG;
+    if (M > 0 && (!dy || !xq || !a_scale)) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(xq) || !aligned16(a_scale) || !aligned16(dw) ||
+        !aligned16(workspace))
+        return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_grad_weight(dy, xq, a_scale, M, N, K, dw, out_dtype, workspace,
+                                                 ws_bytes, as_stream(stream)));
 }
 
 }  // extern "C"

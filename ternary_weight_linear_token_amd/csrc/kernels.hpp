@@ -91,4 +91,49 @@ hipError_t launch_tiled(const int8_t* xq, const float* a_scale, const uint8_t* p
                         const float* w_scale, int64_t M, int64_t N, int64_t K, void* out,
                         int out_dtype, void* workspace, size_t ws_bytes, hipStream_t stream);
 
+// ---- the training side of a layer ----
+// Per-token codes with power-of-two scales, and the bf16 values that any codes stand for.
+hipError_t launch_quant_act_pow2(const uint16_t* x, int64_t M, int64_t K, int8_t* xq,
+                                 float* a_scale, hipStream_t stream);
+hipError_t launch_dequant_act(const int8_t* xq, const float* a_scale, int64_t M, int64_t K,
+                              uint16_t* x, hipStream_t stream);
+
+// Layer norm of (M, K) rows: y, codes xq + a_scale (of the bf16 y; pow2: scale kind), mean and
+// rstd are each optional (NULL); w, b NULL stand for 1 and 0.
+hipError_t launch_layernorm(const uint16_t* x, const float* w, const float* b, float eps,
+                            int64_t M, int64_t K, uint16_t* y, int8_t* xq, float* a_scale,
+                            int pow2, float* mean, float* rstd, hipStream_t stream);
+// Its backward; x bf16, or int8 codes when x_scale is given.  dweight, dbias optional; with
+// either, the workspace of layernorm_back_workspace_size bytes is needed.  M == 0 only
+// clears dweight and dbias.
+size_t layernorm_back_workspace_size(int64_t M, int64_t K);
+hipError_t launch_layernorm_back(const uint16_t* dy, const void* x, const float* x_scale,
+                                 const float* w, const float* mean, const float* rstd, int64_t M,
+                                 int64_t K, uint16_t* dx, float* dweight, float* dbias,
+                                 void* workspace, hipStream_t stream);
+
+// SwiGLU of (M, N) rows, N % 4 == 0: h, codes of h and checkpoints of g and u each optional.
+hipError_t launch_swiglu(const uint16_t* g, const uint16_t* u, int64_t M, int64_t N, uint16_t* h,
+                         int8_t* hq, float* h_scale, int h_pow2, int8_t* gq, float* g_scale,
+                         int8_t* uq, float* u_scale, hipStream_t stream);
+// Its backward; g and u bf16, or int8 codes when the scales are given.
+hipError_t launch_swiglu_back(const uint16_t* dh, const void* g, const float* g_scale,
+                              const void* u, const float* u_scale, int64_t M, int64_t N,
+                              uint16_t* dg, uint16_t* du, hipStream_t stream);
+
+// Gradients of the product: dx (M, K) bf16 from `groups` products that share their input, and
+// dw (N, K) fp32 or bf16.  Workspace optional (fp32 partials of a split contraction).
+// grad_plan: out[0..3] = tile rows, tile columns, k-groups, slices of a call with its workspace
+// (mode 0: dw, I x J = N x K over L[0] = M; mode 1: dx, I x J = M x K over the L[g] = N[g]).
+void grad_plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups, int* out);
+size_t grad_input_workspace_size(int64_t M, int64_t K, int groups, const int64_t* N);
+hipError_t launch_grad_input(const uint16_t* const* dy, const uint8_t* const* packed,
+                             const float* const* w_scale, const int64_t* N, int groups, int64_t M,
+                             int64_t K, uint16_t* dx, void* workspace, size_t ws_bytes,
+                             hipStream_t stream);
+size_t grad_weight_workspace_size(int64_t M, int64_t N, int64_t K);
+hipError_t launch_grad_weight(const uint16_t* dy, const int8_t* xq, const float* a_scale, int64_t M,
+                              int64_t N, int64_t K, void* dw, int out_dtype, void* workspace,
+                              size_t ws_bytes, hipStream_t stream);
+
 }  // namespace bitnet

@@ -1,0 +1,578 @@
+// norm.hip -- layer norm in front of a BitLinear layer (forward, optionally with the int8
+// codes of its output; backward), and the values 8-bit codes stand for, on gfx950.
+//
+//   forward   mu = mean_k x, r = 1 / sqrt(mean_k (x - mu)^2 + eps), y = (x - mu) r w + b
+//             codes: those bitnet_quant_act (or _pow2) gives for the bf16 y
+//   backward  xh = (x - mu) r, g = dy w:
+//             dx = r (g - mean_k g - xh mean_k (g xh)),  dw = sum_m dy xh,  db = sum_m dy
+//             x as bf16 or as an 8-bit checkpoint xq / a.
+//
+// Bound by HBM: x is read once and every output written once.  A row is taken by WPR waves
+// (a "team") of which each lane keeps up to two groups of V elements in registers, so the
+// second pass of the variance and the outputs need no second read; a lane keeps its columns
+// for all rows of its team, so the norm's weight and bias are read once per block and the
+// backward's column sums stay in registers until the block's last row.  Sums are fp32; the
+// variance is the sum of squared differences from the mean (no cancellation).  The column
+// sums are joined block by block in a fixed order by a second launch (no atomics: the same
+// inputs give the same bits).
+#include "device_common.hpp"
+#include "kernels.hpp"
+#include "rows.hpp"
+
+namespace bitnet {
+
+namespace {
+
+constexpr int kTeamGroups = 2;  // groups of V elements a lane holds
+
+struct NormArgs {
+    const uint16_t* x;
+    const float *w, *b;  // NULL: 1 and 0
+    float eps;
+    int64_t M, K;
+    uint16_t* y;     // NULL: not written
+    int8_t* xq;      // NULL: no codes
+    float* a_scale;  // with xq
+    int pow2;
+    float *mean, *rstd;  // NULL: not written
+};
+
+template <int V>
+__device__ __forceinline__ void load_f32(const float* p, int64_t g, float missing, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4 t = p ? reinterpret_cast<const float4*>(p)[(g * V + i) / 4]
+                           : make_float4(missing, missing, missing, missing);
+        v[i] = t.x;
+        v[i + 1] = t.y;
+        v[i + 2] = t.z;
+        v[i + 3] = t.w;
+    }
+}
+
+template <int V, int WPR>
+__global__ __launch_bounds__(64 * WPR) void layernorm_kernel(NormArgs p) {
+    constexpr int G = kTeamGroups, kStride = 64 * WPR;
+    __shared__ float s_red[2][WPR];
+    __shared__ uint32_t s_max[WPR];
+    const int64_t groups = p.K / V;
+    const float K = (float)p.K;
+    float w[G][V], b[G][V];
+    bool in[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const int64_t g = threadIdx.x + (int64_t)i * kStride;
+        in[i] = g < groups;
+        load_f32<V>(p.w, in[i] ? g : 0, 1.0f, w[i]);
+        load_f32<V>(p.b, in[i] ? g : 0, 0.0f, b[i]);
+    }
+    auto load = [&](int64_t m, RowVec<V> (&v)[G]) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            v[i] = zero_row_vec<V>();
+            if (in[i] && m < p.M) v[i] = load_row_vec<V>(p.x + m * p.K, threadIdx.x + (int64_t)i * kStride);
+        }
+    };
+    RowVec<V> cur[G], nxt[G];
+    load(blockIdx.x, cur);
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        load(m + gridDim.x, nxt);
+        float x[G][V], sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            to_f32<V>(cur[i], x[i]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += x[i][j];
+        }
+        const float mean = team_sum<WPR>(sum, s_red[0]) / K;
+        float sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                x[i][j] = in[i] ? x[i][j] - mean : 0.0f;
+                sq += x[i][j] * x[i][j];
+            }
+        const float rstd = 1.0f / sqrtf(team_sum<WPR>(sq, s_red[1]) / K + p.eps);
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j)
+                cur[i].w[j] = f32x2_to_bf16x2_rne(x[i][2 * j] * rstd * w[i][2 * j] + b[i][2 * j],
+                                                  x[i][2 * j + 1] * rstd * w[i][2 * j + 1] + b[i][2 * j + 1]);
+            if (in[i]) {
+                if (p.y) store_row_vec<V>(p.y + m * p.K, threadIdx.x + (int64_t)i * kStride, cur[i]);
+                mx = max_bits<V>(cur[i], mx);
+            }
+        }
+        if (threadIdx.x == 0) {
+            if (p.mean) p.mean[m] = mean;
+            if (p.rstd) p.rstd[m] = rstd;
+        }
+        if (p.xq) {
+            const float a = scale_of(team_max<WPR>(mx, s_max), p.pow2);
+            if (threadIdx.x == 0) p.a_scale[m] = a;
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (in[i]) store_codes<V>(p.xq + m * p.K, threadIdx.x + (int64_t)i * kStride, cur[i], a);
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) cur[i] = nxt[i];
+    }
+}
+
+// Rows too long for a team's registers: one block of 16 waves per row reads it up to four
+// times (the later ones from cache).
+template <int V>
+__global__ __launch_bounds__(1024) void layernorm_long_kernel(NormArgs p) {
+    constexpr int WPR = 16;
+    __shared__ float s_red[2][WPR];
+    __shared__ uint32_t s_max[WPR];
+    const int64_t groups = p.K / V;
+    const float K = (float)p.K;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        const uint16_t* row = p.x + m * p.K;
+        float x[V], sum = 0.0f, sq = 0.0f;
+        for (int64_t g = threadIdx.x; g < groups; g += 1024) {
+            to_f32<V>(load_row_vec<V>(row, g), x);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += x[j];
+        }
+        const float mean = team_sum<WPR>(sum, s_red[0]) / K;
+        for (int64_t g = threadIdx.x; g < groups; g += 1024) {
+            to_f32<V>(load_row_vec<V>(row, g), x);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sq += (x[j] - mean) * (x[j] - mean);
+        }
+        const float rstd = 1.0f / sqrtf(team_sum<WPR>(sq, s_red[1]) / K + p.eps);
+        auto output = [&](int64_t g) {
+            float w[V], b[V];
+            load_f32<V>(p.w, g, 1.0f, w);
+            load_f32<V>(p.b, g, 0.0f, b);
+            to_f32<V>(load_row_vec<V>(row, g), x);
+            RowVec<V> y;
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j)
+                y.w[j] = f32x2_to_bf16x2_rne((x[2 * j] - mean) * rstd * w[2 * j] + b[2 * j],
+                                             (x[2 * j + 1] - mean) * rstd * w[2 * j + 1] + b[2 * j + 1]);
+            return y;
+        };
+        uint32_t mx = 0;
+        for (int64_t g = threadIdx.x; g < groups; g += 1024) {
+            const RowVec<V> y = output(g);
+            if (p.y) store_row_vec<V>(p.y + m * p.K, g, y);
+            mx = max_bits<V>(y, mx);
+        }
+        if (threadIdx.x == 0) {
+            if (p.mean) p.mean[m] = mean;
+            if (p.rstd) p.rstd[m] = rstd;
+        }
+        if (p.xq) {
+            const float a = scale_of(team_max<WPR>(mx, s_max), p.pow2);
+            if (threadIdx.x == 0) p.a_scale[m] = a;
+            for (int64_t g = threadIdx.x; g < groups; g += 1024)
+                store_codes<V>(p.xq + m * p.K, g, output(g), a);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------- backward
+struct NormBackArgs {
+    const uint16_t* dy;
+    const void* x;         // bf16, or int8 codes with x_scale
+    const float* x_scale;  // NULL: x is bf16
+    const float *w, *mean, *rstd;
+    int64_t M, K;
+    uint16_t* dx;
+    float* part;  // (blocks, 2, K) column sums, NULL: not wanted
+};
+
+template <int V, bool CODES>
+struct XVec {
+    RowVec<V> v;
+};
+template <int V>
+struct XVec<V, true> {
+    uint32_t q[V / 4];
+};
+template <int V, bool CODES>
+__device__ __forceinline__ XVec<V, CODES> load_x(const void* x, int64_t row, int64_t g) {
+    XVec<V, CODES> r;
+    if constexpr (CODES) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const int8_t*>(x) + row) + g * (V / 4);
+        if constexpr (V == 8) {
+            const uint2 t = *reinterpret_cast<const uint2*>(p);
+            r.q[0] = t.x;
+            r.q[1] = t.y;
+        } else {
+            r.q[0] = *p;
+        }
+    } else {
+        r.v = load_row_vec<V>(static_cast<const uint16_t*>(x) + row, g);
+    }
+    return r;
+}
+// x - mean: one exact conversion, then (for codes) c * (1 / a) in fp32, exact for a power of two
+template <int V, bool CODES>
+__device__ __forceinline__ void x_to_f32(const XVec<V, CODES>& v, float inv, float (&x)[V]) {
+    if constexpr (CODES) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = (float)(int8_t)(v.q[j / 4] >> (8 * (j & 3))) * inv;
+    } else {
+        to_f32<V>(v.v, x);
+    }
+}
+
+// Blocks of TEAMS teams; the teams of a block walk the rows in step (every wave reaches
+// every barrier; a team past the last row works on zeros).
+template <int V, int WPR, bool CODES>
+__global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void layernorm_back_kernel(NormBackArgs p) {
+    constexpr int G = kTeamGroups, kStride = 64 * WPR, TEAMS = WPR == 16 ? 1 : 8 / WPR;
+    __shared__ float s_red[2][TEAMS][WPR][2];
+    __shared__ float s_join[TEAMS > 1 ? kStride * G * V : 1];
+    const int team = threadIdx.x / kStride, lr = threadIdx.x % kStride;
+    const int64_t groups = p.K / V;
+    const float inv_k = 1.0f / (float)p.K;
+    float w[G][V], dw[G][V], db[G][V];
+    bool in[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const int64_t g = lr + (int64_t)i * kStride;
+        in[i] = g < groups;
+        load_f32<V>(p.w, in[i] ? g : 0, 1.0f, w[i]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = 0.0f;
+    }
+    struct Row {
+        RowVec<V> dy[G];
+        XVec<V, CODES> x[G];
+        float mean, rstd, inv;
+    };
+    auto load = [&](int64_t m, Row& r) {
+        const bool live = m < p.M;
+        r.mean = live ? p.mean[m] : 0.0f;
+        r.rstd = live ? p.rstd[m] : 0.0f;
+        r.inv = 1.0f;
+        if (CODES && live) r.inv = p.x_scale[m];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            r.dy[i] = zero_row_vec<V>();
+            r.x[i] = XVec<V, CODES>{};
+            if (live && in[i]) {
+                const int64_t g = lr + (int64_t)i * kStride;
+                r.dy[i] = load_row_vec<V>(p.dy + m * p.K, g);
+                r.x[i] = load_x<V, CODES>(p.x, m * p.K, g);
+            }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * TEAMS;
+    Row cur, nxt;
+    load((int64_t)blockIdx.x * TEAMS + team, cur);
+    int parity = 0;
+    for (int64_t m0 = (int64_t)blockIdx.x * TEAMS; m0 < p.M; m0 += step, parity ^= 1) {
+        const int64_t m = m0 + team;
+        load(m + step, nxt);
+        const float inv = CODES ? 1.0f / cur.inv : 1.0f;
+        float xh[G][V], g[G][V], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            float d[V];
+            to_f32<V>(cur.dy[i], d);
+            x_to_f32<V, CODES>(cur.x[i], inv, xh[i]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                // columns past the row have dy = 0 and add nothing below
+                xh[i][j] = (xh[i][j] - cur.mean) * cur.rstd;
+                dw[i][j] += d[j] * xh[i][j];
+                db[i][j] += d[j];
+                g[i][j] = d[j] * w[i][j];
+                s1 += g[i][j];
+                s2 += g[i][j] * xh[i][j];
+            }
+        }
+        s1 = wave_sum_f32(s1);
+        s2 = wave_sum_f32(s2);
+        if (WPR > 1) {
+            float(&red)[WPR][2] = s_red[parity][team];
+            if ((threadIdx.x & 63) == 0) {
+                red[lr >> 6][0] = s1;
+                red[lr >> 6][1] = s2;
+            }
+            __syncthreads();
+            s1 = s2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) {
+                s1 += red[i][0];
+                s2 += red[i][1];
+            }
+        }
+        const float c1 = s1 * inv_k, c2 = s2 * inv_k;
+        if (m < p.M) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                RowVec<V> o;
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j)
+                    o.w[j] = f32x2_to_bf16x2_rne(cur.rstd * (g[i][2 * j] - c1 - xh[i][2 * j] * c2),
+                                                 cur.rstd * (g[i][2 * j + 1] - c1 - xh[i][2 * j + 1] * c2));
+                if (in[i]) store_row_vec<V>(p.dx + m * p.K, lr + (int64_t)i * kStride, o);
+            }
+        }
+        cur = nxt;
+    }
+    if (!p.part) return;
+    float* const part = p.part + (int64_t)blockIdx.x * 2 * p.K;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float(&acc)[G][V] = which ? db : dw;
+        for (int tm = 1; tm < TEAMS; ++tm) {
+            __syncthreads();
+            if (team == tm) {
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) s_join[(i * V + j) * kStride + lr] = acc[i][j];
+            }
+            __syncthreads();
+            if (team == 0) {
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[i][j] += s_join[(i * V + j) * kStride + lr];
+            }
+        }
+        if (team == 0) {
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (in[i]) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 4)
+                        *reinterpret_cast<float4*>(part + which * p.K + (lr + (int64_t)i * kStride) * V + j) =
+                            make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+                }
+        }
+    }
+}
+
+// dx of rows too long for a team's registers: one block per row, two reads.
+template <int V, bool CODES>
+__global__ __launch_bounds__(1024) void layernorm_back_long_kernel(NormBackArgs p) {
+    constexpr int WPR = 16;
+    __shared__ float s_red[2][WPR];
+    const int64_t groups = p.K / V;
+    const float inv_k = 1.0f / (float)p.K;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        const float mean = p.mean[m], rstd = p.rstd[m], inv = CODES ? 1.0f / p.x_scale[m] : 1.0f;
+        float xh[V], g[V], s1 = 0.0f, s2 = 0.0f;
+        auto read = [&](int64_t i) {
+            float d[V], w[V];
+            to_f32<V>(load_row_vec<V>(p.dy + m * p.K, i), d);
+            x_to_f32<V, CODES>(load_x<V, CODES>(p.x, m * p.K, i), inv, xh);
+            load_f32<V>(p.w, i, 1.0f, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                xh[j] = (xh[j] - mean) * rstd;
+                g[j] = d[j] * w[j];
+            }
+        };
+        for (int64_t i = threadIdx.x; i < groups; i += 1024) {
+            read(i);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s1 += g[j];
+                s2 += g[j] * xh[j];
+            }
+        }
+        const float c1 = team_sum<WPR>(s1, s_red[0]) * inv_k, c2 = team_sum<WPR>(s2, s_red[1]) * inv_k;
+        for (int64_t i = threadIdx.x; i < groups; i += 1024) {
+            read(i);
+            RowVec<V> o;
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j)
+                o.w[j] = f32x2_to_bf16x2_rne(rstd * (g[2 * j] - c1 - xh[2 * j] * c2),
+                                             rstd * (g[2 * j + 1] - c1 - xh[2 * j + 1] * c2));
+            store_row_vec<V>(p.dx + m * p.K, i, o);
+        }
+    }
+}
+
+// Column sums of such rows: block (c, s) takes 256 columns of every gridDim.y-th row.
+template <bool CODES>
+__global__ __launch_bounds__(256) void layernorm_cols_kernel(NormBackArgs p) {
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (k >= p.K) return;
+    float dw = 0.0f, db = 0.0f;
+    for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
+        const float d = bf16_bits_to_f32(p.dy[m * p.K + k]);
+        float x;
+        if (CODES)
+            x = (float)static_cast<const int8_t*>(p.x)[m * p.K + k] * (1.0f / p.x_scale[m]);
+        else
+            x = bf16_bits_to_f32(static_cast<const uint16_t*>(p.x)[m * p.K + k]);
+        dw += d * ((x - p.mean[m]) * p.rstd[m]);
+        db += d;
+    }
+    float* const part = p.part + (int64_t)blockIdx.y * 2 * p.K;
+    part[k] = dw;
+    part[p.K + k] = db;
+}
+
+// out[k] = sum_b part[b][which][k]: 32 columns per block, eight threads per column, their
+// sums added in order.
+__global__ __launch_bounds__(256) void layernorm_join_kernel(const float* __restrict__ part, int blocks,
+                                                             int64_t K, float* dweight, float* dbias) {
+    __shared__ float s[8][33];
+    const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+    const int64_t k = (int64_t)blockIdx.x * 32 + c;
+    float* const out = blockIdx.y ? dbias : dweight;
+    if (!out) return;
+    float sum = 0.0f;
+    if (k < K)
+        for (int b = r; b < blocks; b += 8) sum += part[((int64_t)b * 2 + blockIdx.y) * K + k];
+    s[r][c] = sum;
+    __syncthreads();
+    if (r == 0 && k < K) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) sum += s[i][c];
+        out[k] = sum;
+    }
+}
+
+// ------------------------------------------------------------------------- dequantize
+// bf16(c / a): eight or four codes a thread, blocks of 256 groups along a row.
+template <int V>
+__global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__ xq,
+                                                      const float* __restrict__ a_scale, int64_t groups,
+                                                      int64_t blocks_per_row, uint16_t* __restrict__ x) {
+    const int64_t m = blockIdx.x / blocks_per_row;
+    const int64_t g = (blockIdx.x - m * blocks_per_row) * 256 + threadIdx.x;
+    if (g >= groups) return;
+    const float a = a_scale[m];
+    float f[V];
+    x_to_f32<V, true>(load_x<V, true>(xq, m * groups * V, g), 1.0f, f);
+    RowVec<V> o;
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) o.w[j] = f32x2_to_bf16x2_rne(f[2 * j] / a, f[2 * j + 1] / a);
+    store_row_vec<V>(x + m * groups * V, g, o);
+}
+
+// Waves per row whose lanes hold the row in two groups each; 0: too long.
+int team_waves(int64_t K, int V) {
+    for (int w = 1; w <= 16; w *= 2)
+        if (K <= (int64_t)w * 64 * kTeamGroups * V) return w;
+    return 0;
+}
+
+// Blocks of the backward pass.
+int64_t back_blocks(int64_t M, int64_t K) {
+    const int w = team_waves(K, K % 8 == 0 ? 8 : 4);
+    if (w == 0) return M < 64 * 32 ? (M + 31) / 32 : 64;
+    const int64_t teams = w == 16 ? 1 : 8 / w;
+    const int64_t b = (M + 2 * teams - 1) / (2 * teams);
+    return b < 512 ? b : 512;
+}
+
+template <int V>
+hipError_t launch_layernorm_v(const NormArgs& a, hipStream_t stream) {
+    const unsigned rows = (unsigned)a.M;
+    switch (team_waves(a.K, V)) {
+        case 1:
+            hipLaunchKernelGGL((layernorm_kernel<V, 1>), dim3(rows < 8192 ? rows : 8192), dim3(64), 0, stream, a);
+            break;
+        case 2:
+            hipLaunchKernelGGL((layernorm_kernel<V, 2>), dim3(rows < 4096 ? rows : 4096), dim3(128), 0, stream, a);
+            break;
+        case 4:
+            hipLaunchKernelGGL((layernorm_kernel<V, 4>), dim3(rows < 2048 ? rows : 2048), dim3(256), 0, stream, a);
+            break;
+        case 8:
+            hipLaunchKernelGGL((layernorm_kernel<V, 8>), dim3(rows < 1024 ? rows : 1024), dim3(512), 0, stream, a);
+            break;
+        case 16:
+            hipLaunchKernelGGL((layernorm_kernel<V, 16>), dim3(rows < 512 ? rows : 512), dim3(1024), 0, stream, a);
+            break;
+        default:
+            hipLaunchKernelGGL((layernorm_long_kernel<V>), dim3(rows < 1024 ? rows : 1024), dim3(1024), 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+template <int V, bool CODES>
+hipError_t launch_back_v(const NormBackArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)back_blocks(a.M, a.K));
+    switch (team_waves(a.K, V)) {
+        case 1:
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 1, CODES>), grid, dim3(512), 0, stream, a);
+            break;
+        case 2:
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 2, CODES>), grid, dim3(512), 0, stream, a);
+            break;
+        case 4:
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 4, CODES>), grid, dim3(512), 0, stream, a);
+            break;
+        case 8:
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 8, CODES>), grid, dim3(512), 0, stream, a);
+            break;
+        case 16:
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 16, CODES>), grid, dim3(1024), 0, stream, a);
+            break;
+        default: {
+            const unsigned rows = (unsigned)(a.M < 1024 ? a.M : 1024);
+            hipLaunchKernelGGL((layernorm_back_long_kernel<V, CODES>), dim3(rows), dim3(1024), 0, stream, a);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess || !a.part) return e;
+            hipLaunchKernelGGL((layernorm_cols_kernel<CODES>), dim3((unsigned)((a.K + 255) / 256), grid.x),
+                               dim3(256), 0, stream, a);
+        }
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_layernorm(const uint16_t* x, const float* w, const float* b, float eps, int64_t M,
+                            int64_t K, uint16_t* y, int8_t* xq, float* a_scale, int pow2, float* mean,
+                            float* rstd, hipStream_t stream) {
+    const NormArgs a = {x, w, b, eps, M, K, y, xq, a_scale, pow2, mean, rstd};
+    return K % 8 == 0 ? launch_layernorm_v<8>(a, stream) : launch_layernorm_v<4>(a, stream);
+}
+
+size_t layernorm_back_workspace_size(int64_t M, int64_t K) {
+    return (size_t)back_blocks(M, K) * 2 * K * 4;
+}
+
+hipError_t launch_layernorm_back(const uint16_t* dy, const void* x, const float* x_scale, const float* w,
+                                 const float* mean, const float* rstd, int64_t M, int64_t K, uint16_t* dx,
+                                 float* dweight, float* dbias, void* workspace, hipStream_t stream) {
+    const bool sums = dweight || dbias;
+    if (M > 0) {
+        const NormBackArgs a = {dy, x, x_scale, w, mean, rstd, M, K, dx,
+                                sums ? static_cast<float*>(workspace) : nullptr};
+        hipError_t e;
+        if (x_scale)
+            e = K % 8 == 0 ? launch_back_v<8, true>(a, stream) : launch_back_v<4, true>(a, stream);
+        else
+            e = K % 8 == 0 ? launch_back_v<8, false>(a, stream) : launch_back_v<4, false>(a, stream);
+        if (e != hipSuccess) return e;
+    }
+    if (!sums) return hipSuccess;
+    hipLaunchKernelGGL(layernorm_join_kernel, dim3((unsigned)((K + 31) / 32), 2), dim3(256), 0, stream,
+                       static_cast<const float*>(workspace), M > 0 ? (int)back_blocks(M, K) : 0, K, dweight,
+                       dbias);
+    return hipGetLastError();
+}
+
+hipError_t launch_dequant_act(const int8_t* xq, const float* a_scale, int64_t M, int64_t K, uint16_t* x,
+                              hipStream_t stream) {
+    const int64_t groups = K / (K % 8 == 0 ? 8 : 4), bpr = (groups + 255) / 256;
+    if (M * bpr > INT32_MAX) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(M * bpr)), block(256);
+    if (K % 8 == 0)
+        hipLaunchKernelGGL(dequant_kernel<8>, grid, block, 0, stream, xq, a_scale, groups, bpr, x);
+    else
+        hipLaunchKernelGGL(dequant_kernel<4>, grid, block, 0, stream, xq, a_scale, groups, bpr, x);
+    return hipGetLastError();
+}
+
+}  // namespace bitnet

@@ -8,6 +8,7 @@
 // (one fused launch) with the per-token absmax scale 127 / max|x|.
 #include "device_common.hpp"
 #include "kernels.hpp"
+#include "rows.hpp"
 
 namespace bitnet {
 
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__
 // MODE 0: per-token scale (both passes).  Per-tensor scale, three launches: MODE 1 runs
 // pass 1 only and leaves the row's max magnitude bits in a_scale[m]; tensor_scale_kernel
 // reduces them and writes the common scale to every a_scale[m]; MODE 2 runs pass 2 with
-// the scale read from a_scale[m].
+// the scale read from a_scale[m].  MODE 3: as MODE 0 with a power-of-two scale.
 template <int V>
 struct QVec {
     uint32_t w[V / 2];  // V bf16 values, two per word, low half first
@@ -203,9 +204,7 @@ __global__ __launch_bounds__(256) void quant_act_kernel(const uint16_t* __restri
             if (live && lr == 0) reinterpret_cast<uint32_t*>(a_scale)[m] = mx;  // bits of max |x|
             return;
         }
-        float amax = bf16_bits_to_f32(mx);
-        amax = amax < 1e-5f ? 1e-5f : amax;
-        a = 127.0f / amax;
+        a = scale_of(mx, MODE == 3);
         if (live && lr == 0) a_scale[m] = a;
     }
 
@@ -377,6 +376,11 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t M, int64_t K, int8_t* xq
 hipError_t launch_quant_act(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, float* a_scale,
                             hipStream_t stream) {
     return launch_quant_rows<0>(x, M, K, xq, a_scale, stream);
+}
+
+hipError_t launch_quant_act_pow2(const uint16_t* x, int64_t M, int64_t K, int8_t* xq,
+                                 float* a_scale, hipStream_t stream) {
+    return launch_quant_rows<3>(x, M, K, xq, a_scale, stream);
 }
 
 hipError_t launch_quant_act_per_tensor(const uint16_t* x, int64_t M, int64_t K, int8_t* xq,
