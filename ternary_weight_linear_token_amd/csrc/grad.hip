@@ -9,10 +9,11 @@
 // 8 bits, so both run on one kernel, MODE choosing the loaders:
 //   MODE 0 (weight): l = m, i = n, j = k.  A = dy rows as they are; B = bf16(xq / a), exact
 //          when a is a power of two.
-//   MODE 1 (input):  l = n, i = m, j = k.  A = bf16(dy * s / 2); B = 2 w, exact (the scale
-//          varies along l, so it has to enter before the sum; rounding dy * s once per
-//          element is independent from element to element, while rounding s itself would
-//          err the same way in every term of rows with nearly equal scales).
+//   MODE 1 (input):  l = n, i = m, j = k.  A = bf16(dy * s); B = 2 w, exact, and the sum
+//          is halved at the end (the scale varies along l, so it has to enter before the sum;
+//          rounding dy * s once per element is independent from element to element, while
+//          rounding s itself would err the same way in every term of rows with nearly equal
+//          scales).
 //
 // Bound: matrix cores for hundreds of tokens and more, the bytes of the weights or of the
 // output below that.
@@ -46,10 +47,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 
-constexpr int kThreads = 512;
-constexpr int kWN = 64;
 // high bytes of bf16(2w) by code (w = code - 1): -2, 0, +2, and 0 for the unused code
 constexpr uint32_t kHi2w = 0x004000C0u;
 
@@ -103,19 +104,18 @@ __device__ __forceinline__ void codes_to_bf16(u32x4 d, float inv, u32x4 (&o)[2])
     }
 }
 
-// 16 packed weights -> 16 bf16 values 2w in order: one lookup gives the high bytes of a
-// field of all four bytes, and the low bytes of -2, 0, 2 are zero.
-__device__ __forceinline__ void weights_to_bf16(uint32_t d, u32x4 (&o)[2]) {
-    uint32_t hi[4];
+// One 2-bit field (bits shift, shift + 1) of 8 bytes -> 8 bf16 values 2w: a lookup gives the
+// high bytes, and the low bytes of -2, 0, 2 are zero.
+__device__ __forceinline__ bf16x8 weights_to_bf16(i32x2 d, int shift) {
+    u32x4 o;
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
-        hi[f] = __builtin_amdgcn_perm(kHi2w, kHi2w, (d >> (2 * f)) & 0x03030303u);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const uint32_t sel = 0x040C000Cu + 0x01000100u * b;
-        o[b >> 1][2 * (b & 1)] = __builtin_amdgcn_perm(hi[1], hi[0], sel);
-        o[b >> 1][2 * (b & 1) + 1] = __builtin_amdgcn_perm(hi[3], hi[2], sel);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t hi =
+            __builtin_amdgcn_perm(kHi2w, kHi2w, ((uint32_t)d[i] >> shift) & 0x03030303u);
+        o[2 * i] = __builtin_amdgcn_perm(0u, hi, 0x010C000Cu);
+        o[2 * i + 1] = __builtin_amdgcn_perm(0u, hi, 0x030C020Cu);
     }
+    return __builtin_bit_cast(bf16x8, o);
 }
 
 // 8 bf16 values times 8 scales, rounded to bf16
@@ -133,6 +133,11 @@ template <int W>
 __device__ __forceinline__ int granule(int l, int c) {
     return l * (2 * W) + ((c ^ (2 * (l & 3))) << 5);
 }
+// Byte offset of 16-byte column c of row l in an [l][W / 4] tile of packed weights.
+template <int W>
+__device__ __forceinline__ int packed_at(int l, int c) {
+    return l * (W / 4) + ((c ^ ((l >> 2) & (W / 64 - 1))) << 4);
+}
 // Byte offset of 16-byte chunk c of row i in an [i][BL] bf16 tile (BL = 32 or 64).
 template <int BL>
 __device__ __forceinline__ int chunk(int i, int c) {
@@ -140,31 +145,36 @@ __device__ __forceinline__ int chunk(int i, int c) {
     return i * (2 * BL) + ((c ^ (CPR == 8 ? (i & 7) : ((i >> 1) & 3))) << 4);
 }
 
-template <int MODE, int BM, int BN, int WM, int G, int BL, bool ALIGNED>
-__global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p) {
-    static_assert((BM / WM) * (BN / kWN) * G == 8, "8 waves");
-    constexpr int TG = kThreads / G;  // threads of a group
-    constexpr int NI = WM / 32, NJ = kWN / 32, KS = BL / 16;
-    constexpr int kA = BM * BL * 2, kB = BN * BL * 2;  // bytes of one stage
+template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, bool ALIGNED>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(GradArgs p) {
+    constexpr int WPG = (BM / WM) * (BN / WN);  // waves of a group
+    constexpr int TG = 64 * WPG;                // threads of a group
+    constexpr int NI = WM / 32, NJ = WN / 32, KS = BL / 16;
+    constexpr int kBRow = MODE == 0 ? 2 * BN : BN / 4;   // bytes of a row of B in LDS
+    constexpr int kA = BM * BL * 2, kB = kBRow * BL;      // bytes of one stage
     constexpr int kBuf = kA + kB;
-    constexpr int kJoin = G > 1 ? (G / 2) * (8 / G) * WM * kWN * 4 : 0;
+    constexpr int kJoin = G > 1 ? (G / 2) * WPG * WM * WN * 4 : 0;
     constexpr int kLds = 2 * G * kBuf > kJoin ? 2 * G * kBuf : kJoin;
     static_assert(kLds <= 160 * 1024, "LDS");
-    // loads of 16 bytes (A), 16 codes or 16 weights (B) per thread and step
+    static_assert(WN == 64 || WN == 128, "columns of a wave");
+    static_assert(KS % 2 == 0, "operand sets alternate");
+    // 16-byte loads of A, 16 codes or 16 weights of B per thread and step
     constexpr int kAUnits = BM * BL / 8, kBUnits = BN * BL / 16;
     constexpr int NA = (kAUnits + TG - 1) / TG, NB = (kBUnits + TG - 1) / TG;
+    constexpr bool kAFull = kAUnits % TG == 0;
+    static_assert(kBUnits % TG == 0, "B units");
+    static_assert(TG % (BL / 8) == 0, "a thread keeps its chunk column");
     __shared__ __align__(1024) uint8_t lds[kLds];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr int WPG = 8 / G;
     const int g = wave / WPG, wg = wave % WPG;
-    const int wi = wg / (BN / kWN), wj = wg % (BN / kWN);
+    const int wi = wg / (BN / WN), wj = wg % (BN / WN);
     const int tg = tid - g * TG;
     uint8_t* const stage = lds + 2 * g * kBuf;
 
     // tile of this block: consecutive blocks go to different XCDs, so each XCD gets a
-    // contiguous run of tiles; runs walk panels of 8 tile rows
+    // contiguous run of tiles; runs walk panels of kPanel tile rows
     const int tiles = p.tiles_i * p.tiles_j, total = tiles * p.slices;
     int t = blockIdx.x;
     {
@@ -181,134 +191,194 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p) {
     const int i0 = ti * BM, j0 = tj * BN;
     const int I = p.I, J = p.J;
 
-    // steps of this block: [s0, s1), group g takes s0 + g, s0 + g + G, ...
+    // steps of this block: [s0, s1), group g takes s0 + g, s0 + g + G, ...; every group runs
+    // nsteps steps and multiplies zeros past its last one
     const int s0 = (int)((int64_t)p.steps * slice / p.slices);
     const int s1 = (int)((int64_t)p.steps * (slice + 1) / p.slices);
     const int nsteps = (s1 - s0 + G - 1) / G;
 
-    u32x4 ra[NA];
-    u32x4 rb[NB];   // MODE 0: 16 codes
-    uint32_t rw[NB];  // MODE 1: 16 weights
-    float rs[MODE == 0 ? NB : 8];
-
-    auto load = [&](int it) {
-        int s = s0 + g + G * it;
+    // ---- loads: the step to load next ----
+    int s_next = s0 + g;  // its index; MODE 1: group q, column l0 of it
+    int q = 0, l0 = 0, L = p.L[0], Lpad = (L + BL - 1) / BL * BL;
+    const uint16_t* pa = p.dy[0];
+    const uint8_t* pb = p.b[0];
+    const float* ps = p.scale[0];
+    const int row_bytes = J / 4;
+    uint32_t voff_a[NA], voff_b[NB];
+    auto offsets_a = [&]() {
+#pragma unroll
+        for (int n = 0; n < NA; ++n) {
+            const int id = tg + n * TG;
+            if constexpr (MODE == 0)
+                voff_a[n] = (uint32_t)(id / (BM / 8) * I + 8 * (id % (BM / 8))) * 2;
+            else
+                voff_a[n] = kAFull || id < kAUnits
+                                ? (uint32_t)(id / (BL / 8) * L + 8 * (id % (BL / 8))) * 2
+                                : 0x80000000u;
+        }
+    };
+    offsets_a();
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
+        voff_b[n] = MODE == 0 ? (uint32_t)(l * J + 16 * c) : (uint32_t)(l * row_bytes + 4 * c);
+    }
+    __amdgpu_buffer_rsrc_t ra, rb, rs;
+    // descriptors of the step s_next (empty ones past the end: they read as zeros)
+    auto locate = [&]() {
         if constexpr (MODE == 0) {
-            const int l0 = s < s1 ? s * BL : p.L[0];
-            const int rows = p.L[0] - l0 < BL ? p.L[0] - l0 : BL;
-            const __amdgpu_buffer_rsrc_t ar =
-                rsrc(p.dy[0] + (int64_t)l0 * I + i0, ((int64_t)rows * I - i0) * 2);
-            const __amdgpu_buffer_rsrc_t br =
-                rsrc(p.b[0] + (int64_t)l0 * J + j0, (int64_t)rows * J - j0);
-            const __amdgpu_buffer_rsrc_t sr = rsrc(p.scale[0] + l0, (int64_t)rows * 4);
-#pragma unroll
-            for (int n = 0; n < NA; ++n) {
-                const int id = tg + n * TG, l = id / (BM / 8), c = id % (BM / 8);
-                const uint32_t off = (uint32_t)(l * I + 8 * c) * 2;
-                ra[n] = ALIGNED ? load16(ar, off) : load8_u16(ar, off);
-            }
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
-                rb[n] = load16(br, (uint32_t)(l * J + 16 * c));
-                rs[n] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sr, 4 * l, 0, 0));
-            }
+            const bool live = s_next < s1;
+            l0 = live ? s_next * BL : 0;
+            const int rows = !live ? 0 : (L - l0 < BL ? L - l0 : BL);
+            ra = rsrc(pa + (int64_t)l0 * I + i0, rows ? ((int64_t)rows * I - i0) * 2 : 0);
+            rb = rsrc(pb + (int64_t)l0 * J + j0, rows ? (int64_t)rows * J - j0 : 0);
+            rs = rsrc(ps + l0, (int64_t)rows * 4);
         } else {
-            int q = 0;
-            if (s >= s1) {
-                q = p.groups;
+            if (l0 >= Lpad) {
+                // past the group's last step: the groups that follow (a dead step stays put)
+                while (q + 1 < p.groups && l0 >= Lpad) {
+                    l0 -= Lpad;
+                    L = p.L[++q];
+                    Lpad = (L + BL - 1) / BL * BL;
+                }
+                pa = p.dy[q];
+                pb = p.b[q];
+                ps = p.scale[q];
+                offsets_a();
+            }
+            const bool live = s_next < s1;
+            const int at = live ? l0 : 0;
+            const int cols = !live ? 0 : (L - at < BL ? L - at : BL);
+            const int rows = I - i0 < BM ? I - i0 : BM;
+            ra = rsrc(pa + (int64_t)i0 * L, live ? (int64_t)rows * L * 2 : 0);
+            rb = rsrc(pb + (int64_t)at * row_bytes + j0 / 4, live ? (int64_t)cols * row_bytes - j0 / 4 : 0);
+            rs = rsrc(ps + at, (int64_t)cols * 4);
+        }
+    };
+    if constexpr (MODE == 1) {
+        l0 = s_next * BL;  // s_next counts the padded steps of all groups
+        // locate() walks to the group
+    }
+
+    u32x4 va[NA];
+    u32x4 vb[NB];      // MODE 0: 16 codes
+    uint32_t vw[NB];   // MODE 1: 16 weights
+    float vs[MODE == 0 ? NB : 8];
+    auto load_a = [&](int n) {
+        if constexpr (MODE == 0) {
+            va[n] = ALIGNED ? load16(ra, voff_a[n]) : load8_u16(ra, voff_a[n]);
+        } else {
+            const int c8 = l0 + 8 * (tg % (BL / 8));  // columns past the row's end read as zeros
+            if (ALIGNED) {
+                va[n] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, c8 < L ? voff_a[n] : 0x80000000u, 2 * l0, 0));
             } else {
-                while (s >= (p.L[q] + BL - 1) / BL) s -= (p.L[q++] + BL - 1) / BL;
-            }
-            const bool live = q < p.groups;
-            if (!live) q = 0;
-            const int L = p.L[q];
-            const int l0 = live ? s * BL : L;
-            const int cols = L - l0 < BL ? L - l0 : BL;
-            const int row_bytes = J / 4;
-            const __amdgpu_buffer_rsrc_t ar =
-                rsrc(p.dy[q] + (int64_t)i0 * L, live ? (int64_t)(I - i0 < BM ? I - i0 : BM) * L * 2 : 0);
-            const __amdgpu_buffer_rsrc_t br =
-                rsrc(p.b[q] + (int64_t)l0 * row_bytes + j0 / 4, (int64_t)cols * row_bytes - j0 / 4);
-            const __amdgpu_buffer_rsrc_t sr = rsrc(p.scale[q] + l0, (int64_t)cols * 4);
-            {
-                const int c = tg % (BL / 8);
-                const u32x4 a0 = load16(sr, 32 * c), a1 = load16(sr, 32 * c + 16);
+                u32x4 v;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    rs[e] = 0.5f * __uint_as_float(a0[e]);
-                    rs[4 + e] = 0.5f * __uint_as_float(a1[e]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(
+                        ra, c8 + 2 * i < L ? voff_a[n] + 4 * i : 0x80000000u, 2 * l0, 0);
+                    const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(
+                        ra, c8 + 2 * i + 1 < L ? voff_a[n] + 4 * i + 2 : 0x80000000u, 2 * l0, 0);
+                    v[i] = (lo & 0xFFFFu) | (hi << 16);
                 }
-            }
-#pragma unroll
-            for (int n = 0; n < NA; ++n) {
-                const int id = tg + n * TG, i = id / (BL / 8), c = id % (BL / 8);
-                const uint32_t off = (uint32_t)(i * L + l0 + 8 * c) * 2;
-                if (kAUnits % TG == 0 || id < kAUnits) ra[n] = ALIGNED ? load16(ar, off) : load8_u16(ar, off);
-                if (cols < BL) {  // the last step of a group: columns past the end are zero
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (8 * c + 2 * e >= cols) ra[n][e] = 0u;
-                        else if (8 * c + 2 * e + 1 >= cols) ra[n][e] &= 0xFFFFu;
-                    }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
-                const uint32_t off = (uint32_t)(l * row_bytes + 4 * c);
-                if (ALIGNED) {
-                    rw[n] = __builtin_amdgcn_raw_buffer_load_b32(br, off, 0, 0);
-                } else {
-                    uint32_t d = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        d |= ((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(br, off + e, 0, 0) & 0xFFu) << (8 * e);
-                    rw[n] = d;
-                }
+                va[n] = v;
             }
         }
     };
-
-    auto store = [&](int it, int buf) {
-        uint8_t* const A = stage + buf * kBuf;
-        uint8_t* const B = A + kA;
+    auto load_b = [&](int n) {
         if constexpr (MODE == 0) {
-            const int s = s0 + g + G * it;
-            const int rows = s < s1 ? p.L[0] - s * BL : 0;
-#pragma unroll
-            for (int n = 0; n < NA; ++n) {
-                const int id = tg + n * TG, l = id / (BM / 8), c = id % (BM / 8);
-                *reinterpret_cast<u32x4*>(A + granule<BM>(l, c >> 1) + 16 * (c & 1)) = ra[n];
-            }
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
-                u32x4 o[2];
-                codes_to_bf16(rb[n], l < rows ? 1.0f / rs[n] : 0.0f, o);
-                u32x4* const dst = reinterpret_cast<u32x4*>(B + granule<BN>(l, c));
-                dst[0] = o[0];
-                dst[1] = o[1];
-            }
+            vb[n] = load16(rb, voff_b[n]);
+            vs[n] = __builtin_bit_cast(
+                float, __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * ((tg + n * TG) / (BN / 16)), 0, 0));
+        } else if (ALIGNED) {
+            vw[n] = __builtin_amdgcn_raw_buffer_load_b32(rb, voff_b[n], 0, 0);
         } else {
+            uint32_t d = 0;
 #pragma unroll
-            for (int n = 0; n < NA; ++n) {
-                const int id = tg + n * TG, i = id / (BL / 8), c = id % (BL / 8);
-                if (kAUnits % TG == 0 || id < kAUnits)
-                    *reinterpret_cast<u32x4*>(A + chunk<BL>(i, c)) = scaled_bf16(ra[n], rs);
-            }
+            for (int e = 0; e < 4; ++e)
+                d |= ((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rb, voff_b[n] + e, 0, 0) & 0xFFu) << (8 * e);
+            vw[n] = d;
+        }
+    };
+    auto load_s = [&]() {
+        if constexpr (MODE == 1) {
+            const u32x4 a0 = load16(rs, 32 * (tg % (BL / 8))), a1 = load16(rs, 32 * (tg % (BL / 8)) + 16);
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
-                u32x4 o[2];
-                weights_to_bf16(rw[n], o);
-                u32x4* const dst = reinterpret_cast<u32x4*>(B + granule<BN>(l, c));
-                dst[0] = o[0];
-                dst[1] = o[1];
+            for (int e = 0; e < 4; ++e) {
+                vs[e] = __uint_as_float(a0[e]);
+                vs[4 + e] = __uint_as_float(a1[e]);
             }
         }
     };
 
+    // ---- conversion into an LDS stage ----
+    auto store_a = [&](int n, uint8_t* A) {
+        const int id = tg + n * TG;
+        if constexpr (MODE == 0) {
+            const int l = id / (BM / 8), c = id % (BM / 8);
+            *reinterpret_cast<u32x4*>(A + granule<BM>(l, c >> 1) + 16 * (c & 1)) = va[n];
+        } else {
+            if (kAFull || id < kAUnits)
+                *reinterpret_cast<u32x4*>(A + chunk<BL>(id / (BL / 8), id % (BL / 8))) = scaled_bf16(va[n], vs);
+        }
+    };
+    auto store_b = [&](int n, uint8_t* B) {
+        const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
+        if constexpr (MODE == 0) {
+            u32x4 o[2];
+            codes_to_bf16(vb[n], vs[n] > 0.0f ? 1.0f / vs[n] : 0.0f, o);  // rows past the end: scale 0
+            u32x4* const dst = reinterpret_cast<u32x4*>(B + granule<BN>(l, c));
+            dst[0] = o[0];
+            dst[1] = o[1];
+        } else {
+            *reinterpret_cast<uint32_t*>(B + packed_at<BN>(l, c >> 2) + 4 * (c & 3)) = vw[n];
+        }
+    };
+
+    // ---- operands ----
+    const int t16 = lane & 15, half = (lane >> 4) & 1, l8 = 8 * (lane >> 5);
+    int off_a[MODE == 0 ? NI : KS], off_b[NJ];
+    if constexpr (MODE == 0) {
+        // 16-bit transposed reads: row l8 + t16 / 4, 8 bytes t16 % 4 of the granule
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            off_a[i] = granule<BM>(l8 + (t16 >> 2), (wi * WM + 32 * i) / 16 + half) + 8 * (t16 & 3);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            off_b[j] = granule<BN>(l8 + (t16 >> 2), (wj * WN + 32 * j) / 16 + half) + 8 * (t16 & 3);
+    } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            off_a[ks] = chunk<BL>(wi * WM + (lane & 31), 2 * ks + (lane >> 5));
+        // 8-bit transposed reads: row l8 + t16 / 2, 8 bytes t16 % 2 of a 16-byte column.  WN 64:
+        // both halves of the lanes read the wave's 16 byte columns; WN 128: one 16 each.
+        off_b[0] = packed_at<BN>(l8 + (t16 >> 1), WN == 64 ? wj : 2 * wj + half) + 8 * (t16 & 1);
+    }
+    auto tr16 = [&](const uint8_t* a, int rows4) {
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + rows4));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    struct Operands {
+        bf16x8 a[NI];
+        bf16x8 b[MODE == 0 ? NJ : 1];  // MODE 0
+        i32x2 w;                       // MODE 1: byte column of 8 rows
+    };
+    auto read = [&](const uint8_t* A, int ks, Operands& o) {
+        const uint8_t* const B = A + kA;
+        if constexpr (MODE == 0) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) o.b[j] = tr16(B + off_b[j] + ks * 16 * kBRow, 4 * kBRow);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) o.a[i] = tr16(A + off_a[i] + ks * 16 * 2 * BM, 8 * BM);
+        } else {
+            o.w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(B + off_b[0] + ks * 16 * kBRow));
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                o.a[i] = *reinterpret_cast<const bf16x8*>(A + off_a[ks] + i * 32 * 2 * BL);
+        }
+    };
     f32x16 acc[NI][NJ];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
@@ -316,74 +386,85 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p) {
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-    // lane's part of a transposed read: row 8 (lane / 32) + (t / 4) of a 16-row step, 8 bytes
-    // t % 4 of the granule of its 16 columns
-    const int t16 = lane & 15, half = (lane >> 4) & 1, l8 = 8 * (lane >> 5) + (t16 >> 2);
-    auto tr_read = [&](const uint8_t* tile, int off, int row_bytes) {
-        const uint8_t* a = tile + off;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * row_bytes));
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
-        const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        return __builtin_bit_cast(bf16x8, v);
-    };
-    int offA[NI], offB[NJ];
+    auto multiply = [&](const Operands& o) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        if constexpr (MODE == 0)
-            offA[i] = granule<BM>(l8, (wi * WM + 32 * i) / 16 + half) + 8 * (t16 & 3);
-        else
-            offA[i] = 0;
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-        offB[j] = granule<BN>(l8, (wj * kWN + 32 * j) / 16 + half) + 8 * (t16 & 3);
-
-    auto multiply = [&](int buf) {
-        const uint8_t* const A = stage + buf * kBuf;
-        const uint8_t* const B = A + kA;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            bf16x8 a[NI], b[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) b[j] = tr_read(B, offB[j] + ks * 16 * 2 * BN, 2 * BN);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                if constexpr (MODE == 0)
-                    a[i] = tr_read(A, offA[i] + ks * 16 * 2 * BM, 2 * BM);
-                else
-                    a[i] = *reinterpret_cast<const bf16x8*>(
-                        A + chunk<BL>(wi * WM + 32 * i + (lane & 31), 2 * ks + (lane >> 5)));
-            }
+        for (int j = 0; j < NJ; ++j) {
+            bf16x8 b;
+            if constexpr (MODE == 0)
+                b = o.b[j];
+            else  // field 2 j + half (WN 64) or j (WN 128) of the byte column
+                b = weights_to_bf16(o.w, WN == 64 ? 4 * j + 2 * half : 2 * j);
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.a[i], b, acc[i][j], 0, 0, 0);
         }
     };
 
-    if (nsteps > 0) {
-        load(0);
-        store(0, 0);
-    }
+    // Step it multiplies stage it % 2 while the registers' step it + 1 is converted into the
+    // other stage, spread over all but the last 16 rows' products, and each register is
+    // refilled for step it + 2 as soon as it is free: a load has a whole step to arrive.  One
+    // barrier before the last products of the step, whose operands are already in registers;
+    // the first operands of step it + 1 are read behind it.
+    constexpr int P = KS - 1;  // parts of a conversion
+    auto convert = [&](int part, uint8_t* A) {
+#pragma unroll
+        for (int n = 0; n < NA; ++n)
+            if (n * P / NA == part) store_a(n, A);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            if ((NB - 1 - n) * P / NB == part) store_b(n, A + kA);
+    };
+    auto refill = [&](int part) {
+#pragma unroll
+        for (int n = 0; n < NA; ++n)
+            if (n * P / NA == part) load_a(n);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            if ((NB - 1 - n) * P / NB == part) load_b(n);
+        if (part == P - 1) load_s();
+    };
+    auto advance = [&]() {
+        s_next += G;
+        l0 += G * BL;
+        locate();
+    };
+    Operands op[2];
+    locate();
+#pragma unroll
+    for (int part = 0; part < P; ++part) refill(part);
+    advance();
+#pragma unroll
+    for (int part = 0; part < P; ++part) convert(part, stage);
+#pragma unroll
+    for (int part = 0; part < P; ++part) refill(part);
     __syncthreads();
+    read(stage, 0, op[0]);
     for (int it = 0; it < nsteps; ++it) {
-        const bool more = it + 1 < nsteps;
-        if (more) load(it + 1);
-        multiply(it & 1);
-        if (more) store(it + 1, (it + 1) & 1);
-        __syncthreads();
+        uint8_t* const cur = stage + (it & 1) * kBuf;
+        uint8_t* const nxt = stage + ((it + 1) & 1) * kBuf;
+        advance();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks < KS - 1) {
+                read(cur, ks + 1, op[(ks + 1) & 1]);
+                convert(ks, nxt);
+                refill(ks);
+            } else {
+                __syncthreads();
+                read(nxt, 0, op[0]);
+            }
+            multiply(op[ks & 1]);
+        }
     }
 
     // join the groups: the upper half of the remaining groups hands its sums to the lower
-    if (G > 1) {
+    if constexpr (G > 1) {
         float* const x = reinterpret_cast<float*>(lds);
+        __syncthreads();
 #pragma unroll
         for (int h = G / 2; h >= 1; h /= 2) {
             if (g >= h && g < 2 * h) {
-                float* const w = x + ((g - h) * WPG + wg) * (WM * kWN) + lane;
+                float* const w = x + ((g - h) * WPG + wg) * (WM * WN) + lane;
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -393,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p) {
             }
             __syncthreads();
             if (g < h) {
-                const float* const w = x + (g * WPG + wg) * (WM * kWN) + lane;
+                const float* const w = x + (g * WPG + wg) * (WM * WN) + lane;
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -406,23 +487,54 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p) {
         if (g > 0) return;
     }
 
-    // lane l, register r of a 32x32 accumulator: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+    // lane l, register r of a 32x32 accumulator: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
+    // MODE 0: block j holds columns 32 j + l % 32.  MODE 1: byte column l % 16 (WN 64) or l % 32
+    // (WN 128) of the wave, its weight 2 j + half or j.
+    float* const part = p.part + (int64_t)slice * I * J;
+    const int jw = j0 + wj * WN;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int col = j0 + wj * kWN + 32 * j + (lane & 31);
+        for (int r = 0; r < 16; ++r) {
+            const int row = i0 + wi * WM + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+            const int64_t o = (int64_t)row * J;
+            if constexpr (MODE == 0) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = i0 + wi * WM + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                for (int j = 0; j < NJ; ++j) {
+                    const int col = jw + 32 * j + (lane & 31);
+                    if (row < I && col < J) {
+                        if (p.slices > 1)
+                            part[o + col] = acc[i][j][r];
+                        else if (p.out_dtype == BITNET_OUT_F32)
+                            static_cast<float*>(p.out)[o + col] = acc[i][j][r];
+                        else
+                            static_cast<uint16_t*>(p.out)[o + col] = f32_to_bf16_rne(acc[i][j][r]);
+                    }
+                }
+            } else if constexpr (WN == 64) {
+                // lanes l and l + 16 hold columns 4 t + (0, 2) and 4 t + (1, 3): exchange, so that a
+                // lane has two neighbours, 4 t + 2 half + (0, 1)
+                const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][0][r]),
+                                                                __float_as_uint(acc[i][1][r]), false, false);
+                const float v0 = 0.5f * __uint_as_float(x[0]), v1 = 0.5f * __uint_as_float(x[1]);
+                const int col = jw + 4 * t16 + 2 * half;
                 if (row < I && col < J) {
-                    const int64_t o = (int64_t)row * J + col;
                     if (p.slices > 1)
-                        p.part[(int64_t)slice * I * J + o] = acc[i][j][r];
-                    else if (p.out_dtype == BITNET_OUT_F32)
-                        static_cast<float*>(p.out)[o] = acc[i][j][r];
+                        *reinterpret_cast<float2*>(part + o + col) = make_float2(v0, v1);
                     else
-                        static_cast<uint16_t*>(p.out)[o] = f32_to_bf16_rne(acc[i][j][r]);
+                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o + col) =
+                            f32x2_to_bf16x2_rne(v0, v1);
+                }
+            } else {
+                const int col = jw + 4 * (lane & 31);
+                const float4 v = make_float4(0.5f * acc[i][0][r], 0.5f * acc[i][1][r],
+                                             0.5f * acc[i][2][r], 0.5f * acc[i][3][r]);
+                if (row < I && col < J) {
+                    if (p.slices > 1)
+                        *reinterpret_cast<float4*>(part + o + col) = v;
+                    else
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o + col) =
+                            make_uint2(f32x2_to_bf16x2_rne(v.x, v.y), f32x2_to_bf16x2_rne(v.z, v.w));
                 }
             }
         }
@@ -453,9 +565,12 @@ struct GradPlan {
     int cfg, slices, steps;
 };
 struct GradCfg {
-    int bm, bn, wm, g, bl;
+    int bm, bn, wm, wn, g, bl;
 };
-constexpr GradCfg kCfg[] = {{256, 256, 128, 1, 64}, {256, 128, 128, 2, 32}, {128, 128, 128, 4, 32}, {32, 256, 32, 2, 32}};
+constexpr GradCfg kCfg[] = {{256, 256, 128, 64, 1, 64},
+                            {256, 128, 128, 64, 2, 32},
+                            {128, 128, 128, 64, 4, 32},
+                            {32, 256, 32, 64, 2, 32}};
 
 GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
     GradPlan best = {0, 1, 0};
@@ -487,11 +602,11 @@ GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
 template <int MODE, int C>
 void launch_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
     constexpr GradCfg k = kCfg[C];
-    const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices)), block(kThreads);
+    const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices)), block(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g);
     if (aligned)
-        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.g, k.bl, true>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, true>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.g, k.bl, false>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, false>), grid, block, 0, stream, a);
 }
 
 hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, void* workspace,
@@ -559,7 +674,7 @@ hipError_t launch_grad_input(const uint16_t* const* dy, const uint8_t* const* pa
         a.scale[a.groups] = w_scale[q];
         a.L[a.groups] = (int)N[q];
         L[a.groups++] = N[q];
-        aligned = aligned && N[q] % 2 == 0;
+        aligned = aligned && N[q] % 8 == 0;
     }
     a.I = (int)M;
     a.J = (int)K;

@@ -368,15 +368,15 @@ def test_swiglu_gradient_against_differences():
 # --------------------------------------------------------------------- product gradients
 
 def check_grad_input(dys, packs, scales, K, got, what):
-    """Against the sum of the kernel's operands (dy * s / 2 rounded to bf16, 2 w) in 64 bits:
+    """Against the sum of the kernel's operands (dy * s rounded to bf16, w) in 64 bits:
     what remains is the fp32 sum and the output's rounding; and against the exact sum."""
     ref = exact = size = 0.0
     n = 0
     for dy, p, s in zip(dys, packs, scales):
         w = bw.unpack_weights(p, K).double()
-        a = (dy.float() * (0.5 * s)).to(torch.bfloat16).double()
-        ref = ref + a @ (2 * w)
-        size = size + a.abs() @ (2 * w).abs()
+        a = (dy.float() * s).to(torch.bfloat16).double()
+        ref = ref + a @ w
+        size = size + a.abs() @ w.abs()
         exact = exact + (dy.double() * s.double()) @ w
         n += dy.shape[1]
     close(got, ref, BF * ref.abs() + (n + 64) * U * size + TINY, what)
