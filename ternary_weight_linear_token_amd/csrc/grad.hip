@@ -34,8 +34,10 @@
 //  * Few output tiles: l is also split over blocks (slices); every slice writes fp32 partial
 //    sums to the workspace and a second launch adds them in a fixed order.
 //  * Tails: rows past the end of l read as zeros through the buffer descriptors' bounds or a
-//    mask; columns past i or j are computed from whatever lies there and never stored (they
+//    mask; rows that start off a dword are put together from the dwords around them; columns past i or j are computed from whatever lies there and never stored (they
 //    only reach their own outputs).
+#include <utility>
+
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -76,55 +78,18 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
-// 8 bf16 values at a 2-byte aligned offset (rows of odd length)
-__device__ __forceinline__ u32x4 load8_u16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(r, off + 4 * i, 0, 0);
-        const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(r, off + 4 * i + 2, 0, 0);
-        v[i] = (lo & 0xFFFFu) | (hi << 16);
-    }
-    return v;
-}
-
-// 16 int8 codes -> 16 bf16 values c * inv (one rounding each; exact for a power of two):
-// c + 128 as an unsigned byte is exact in fp32, and so is 128 inv.
-__device__ __forceinline__ void codes_to_bf16(u32x4 d, float inv, u32x4 (&o)[2]) {
-    const float off = -128.0f * inv;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t u = d[i] ^ 0x80808080u;
-        const float f0 = __builtin_fmaf((float)(u & 0xFFu), inv, off);
-        const float f1 = __builtin_fmaf((float)((u >> 8) & 0xFFu), inv, off);
-        const float f2 = __builtin_fmaf((float)((u >> 16) & 0xFFu), inv, off);
-        const float f3 = __builtin_fmaf((float)(u >> 24), inv, off);
-        o[i >> 1][2 * (i & 1)] = f32x2_to_bf16x2_rne(f0, f1);
-        o[i >> 1][2 * (i & 1) + 1] = f32x2_to_bf16x2_rne(f2, f3);
-    }
-}
-
-// One 2-bit field (bits shift, shift + 1) of 8 bytes -> 8 bf16 values 2w: a lookup gives the
-// high bytes, and the low bytes of -2, 0, 2 are zero.
-__device__ __forceinline__ bf16x8 weights_to_bf16(i32x2 d, int shift) {
+// 8 bf16 values at a 2-byte aligned offset (rows of odd length): the aligned dwords around
+// them, shifted together.  The descriptors end on a whole dword.
+__device__ __forceinline__ u32x4 load8_half(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff) {
+    const u32x4 v =
+        __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off & ~3u, soff, 0));
+    const uint32_t x = __builtin_amdgcn_raw_buffer_load_b32(r, (off & ~3u) + 16, soff, 0);
+    const uint32_t sh = 8 * (off & 2);
     u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t hi =
-            __builtin_amdgcn_perm(kHi2w, kHi2w, ((uint32_t)d[i] >> shift) & 0x03030303u);
-        o[2 * i] = __builtin_amdgcn_perm(0u, hi, 0x010C000Cu);
-        o[2 * i + 1] = __builtin_amdgcn_perm(0u, hi, 0x030C020Cu);
-    }
-    return __builtin_bit_cast(bf16x8, o);
-}
-
-// 8 bf16 values times 8 scales, rounded to bf16
-__device__ __forceinline__ u32x4 scaled_bf16(u32x4 v, const float (&s)[8]) {
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = f32x2_to_bf16x2_rne(__uint_as_float(v[i] << 16) * s[2 * i],
-                                   __uint_as_float(v[i] & 0xFFFF0000u) * s[2 * i + 1]);
+    o[0] = __builtin_amdgcn_alignbit(v[1], v[0], sh);
+    o[1] = __builtin_amdgcn_alignbit(v[2], v[1], sh);
+    o[2] = __builtin_amdgcn_alignbit(v[3], v[2], sh);
+    o[3] = __builtin_amdgcn_alignbit(x, v[3], sh);
     return o;
 }
 
@@ -145,7 +110,7 @@ __device__ __forceinline__ int chunk(int i, int c) {
     return i * (2 * BL) + ((c ^ (CPR == 8 ? (i & 7) : ((i >> 1) & 3))) << 4);
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, bool ALIGNED>
+template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, int D, bool ALIGNED>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(GradArgs p) {
     constexpr int WPG = (BM / WM) * (BN / WN);  // waves of a group
     constexpr int TG = 64 * WPG;                // threads of a group
@@ -224,13 +189,15 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
         voff_b[n] = MODE == 0 ? (uint32_t)(l * J + 16 * c) : (uint32_t)(l * row_bytes + 4 * c);
     }
     __amdgpu_buffer_rsrc_t ra, rb, rs;
+    // the last element of rows at odd places lies in a dword that the descriptor has to cover
+    auto whole = [](int64_t bytes) { return ALIGNED ? bytes : (bytes + 3) & ~(int64_t)3; };
     // descriptors of the step s_next (empty ones past the end: they read as zeros)
     auto locate = [&]() {
         if constexpr (MODE == 0) {
             const bool live = s_next < s1;
             l0 = live ? s_next * BL : 0;
             const int rows = !live ? 0 : (L - l0 < BL ? L - l0 : BL);
-            ra = rsrc(pa + (int64_t)l0 * I + i0, rows ? ((int64_t)rows * I - i0) * 2 : 0);
+            ra = rsrc(pa + (int64_t)l0 * I + i0, rows ? whole(((int64_t)rows * I - i0) * 2) : 0);
             rb = rsrc(pb + (int64_t)l0 * J + j0, rows ? (int64_t)rows * J - j0 : 0);
             rs = rsrc(ps + l0, (int64_t)rows * 4);
         } else {
@@ -250,8 +217,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
             const int at = live ? l0 : 0;
             const int cols = !live ? 0 : (L - at < BL ? L - at : BL);
             const int rows = I - i0 < BM ? I - i0 : BM;
-            ra = rsrc(pa + (int64_t)i0 * L, live ? (int64_t)rows * L * 2 : 0);
-            rb = rsrc(pb + (int64_t)at * row_bytes + j0 / 4, live ? (int64_t)cols * row_bytes - j0 / 4 : 0);
+            ra = rsrc(pa + (int64_t)i0 * L, live ? whole((int64_t)rows * L * 2) : 0);
+            rb = rsrc(pb + (int64_t)at * row_bytes + j0 / 4,
+                      live ? whole((int64_t)cols * row_bytes - j0 / 4) : 0);
             rs = rsrc(ps + at, (int64_t)cols * 4);
         }
     };
@@ -260,80 +228,98 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
         // locate() walks to the group
     }
 
-    u32x4 va[NA];
-    u32x4 vb[NB];      // MODE 0: 16 codes
-    uint32_t vw[NB];   // MODE 1: 16 weights
-    float vs[MODE == 0 ? NB : 8];
-    auto load_a = [&](int n) {
+    struct Loads {
+        u32x4 a[NA];
+        u32x4 b[MODE == 0 ? NB : 1];     // 16 codes each
+        uint32_t w[MODE == 1 ? NB : 1];  // 16 weights each
+        float s[MODE == 0 ? NB : 8];
+        int left;  // MODE 1: elements of the row chunks that are inside their rows
+    };
+    Loads ld[D];
+    auto load_a = [&](Loads& v, int n) {
         if constexpr (MODE == 0) {
-            va[n] = ALIGNED ? load16(ra, voff_a[n]) : load8_u16(ra, voff_a[n]);
+            v.a[n] = ALIGNED ? load16(ra, voff_a[n]) : load8_half(ra, voff_a[n], 0);
         } else {
-            const int c8 = l0 + 8 * (tg % (BL / 8));  // columns past the row's end read as zeros
-            if (ALIGNED) {
-                va[n] = __builtin_bit_cast(
-                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, c8 < L ? voff_a[n] : 0x80000000u, 2 * l0, 0));
+            if (ALIGNED) {  // whole chunks: those past the row's end read as zeros
+                const bool in = l0 + 8 * (tg % (BL / 8)) < L;
+                v.a[n] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? voff_a[n] : 0x80000000u, 2 * l0, 0));
             } else {
-                u32x4 v;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(
-                        ra, c8 + 2 * i < L ? voff_a[n] + 4 * i : 0x80000000u, 2 * l0, 0);
-                    const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(
-                        ra, c8 + 2 * i + 1 < L ? voff_a[n] + 4 * i + 2 : 0x80000000u, 2 * l0, 0);
-                    v[i] = (lo & 0xFFFFu) | (hi << 16);
-                }
-                va[n] = v;
+                v.a[n] = load8_half(ra, voff_a[n], 2 * l0);
             }
         }
     };
-    auto load_b = [&](int n) {
+    auto load_b = [&](Loads& v, int n) {
         if constexpr (MODE == 0) {
-            vb[n] = load16(rb, voff_b[n]);
-            vs[n] = __builtin_bit_cast(
+            v.b[n] = load16(rb, voff_b[n]);
+            v.s[n] = __builtin_bit_cast(
                 float, __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * ((tg + n * TG) / (BN / 16)), 0, 0));
         } else if (ALIGNED) {
-            vw[n] = __builtin_amdgcn_raw_buffer_load_b32(rb, voff_b[n], 0, 0);
+            v.w[n] = __builtin_amdgcn_raw_buffer_load_b32(rb, voff_b[n], 0, 0);
         } else {
-            uint32_t d = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                d |= ((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rb, voff_b[n] + e, 0, 0) & 0xFFu) << (8 * e);
-            vw[n] = d;
+            // rows at any byte: the two dwords around the four bytes
+            const auto d = __builtin_amdgcn_raw_buffer_load_b64(rb, voff_b[n] & ~3u, 0, 0);
+            v.w[n] = __builtin_amdgcn_alignbit(d[1], d[0], 8 * (voff_b[n] & 3));
         }
     };
-    auto load_s = [&]() {
+    auto load_s = [&](Loads& v) {
         if constexpr (MODE == 1) {
             const u32x4 a0 = load16(rs, 32 * (tg % (BL / 8))), a1 = load16(rs, 32 * (tg % (BL / 8)) + 16);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                vs[e] = __uint_as_float(a0[e]);
-                vs[4 + e] = __uint_as_float(a1[e]);
+                v.s[e] = __uint_as_float(a0[e]);
+                v.s[4 + e] = __uint_as_float(a1[e]);
             }
+            v.left = L - l0 - 8 * (tg % (BL / 8));
         }
     };
 
-    // ---- conversion into an LDS stage ----
-    auto store_a = [&](int n, uint8_t* A) {
+    // ---- conversion into an LDS stage, in slices of a few vector instructions ----
+    // MODE 0: unit n of B in nine slices, the row's 1 / a and then two codes of each dword at a
+    // time; A goes to LDS as it is.  MODE 1: one dword of a chunk of A per slice; B as it is.
+    constexpr int kSlices = MODE == 0 ? NB * 9 : NA * 4;
+    float inv = 0.0f;      // MODE 0
+    u32x4 half_out[2];     // MODE 0: the unit's 16 values
+    auto write_a = [&](const Loads& v, int n, uint8_t* A) {
         const int id = tg + n * TG;
         if constexpr (MODE == 0) {
             const int l = id / (BM / 8), c = id % (BM / 8);
-            *reinterpret_cast<u32x4*>(A + granule<BM>(l, c >> 1) + 16 * (c & 1)) = va[n];
-        } else {
-            if (kAFull || id < kAUnits)
-                *reinterpret_cast<u32x4*>(A + chunk<BL>(id / (BL / 8), id % (BL / 8))) = scaled_bf16(va[n], vs);
+            *reinterpret_cast<u32x4*>(A + granule<BM>(l, c >> 1) + 16 * (c & 1)) = v.a[n];
+        } else if (kAFull || id < kAUnits) {
+            *reinterpret_cast<u32x4*>(A + chunk<BL>(id / (BL / 8), id % (BL / 8))) = v.a[n];
         }
     };
-    auto store_b = [&](int n, uint8_t* B) {
-        const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
+    auto convert_slice = [&](Loads& v, int i, uint8_t* A) {
         if constexpr (MODE == 0) {
-            u32x4 o[2];
-            codes_to_bf16(vb[n], vs[n] > 0.0f ? 1.0f / vs[n] : 0.0f, o);  // rows past the end: scale 0
-            u32x4* const dst = reinterpret_cast<u32x4*>(B + granule<BN>(l, c));
-            dst[0] = o[0];
-            dst[1] = o[1];
+            const int n = i / 9, h = i % 9 - 1;
+            if (h < 0) {
+                inv = v.s[n] > 0.0f ? 1.0f / v.s[n] : 0.0f;  // rows past the end: scale 0
+            } else {
+                // (c + 128) inv - 128 inv: a byte and 128 inv are exact in fp32, so each value
+                // is rounded once (not at all for a power of two)
+                const uint32_t u = (v.b[n][h >> 1] ^ 0x80808080u) >> (16 * (h & 1));
+                const float off = -128.0f * inv;
+                half_out[h >> 2][h & 3] = f32x2_to_bf16x2_rne(__builtin_fmaf((float)(u & 0xFFu), inv, off),
+                                                              __builtin_fmaf((float)((u >> 8) & 0xFFu), inv, off));
+            }
+            if (h == 7) {
+                const int id = tg + n * TG;
+                u32x4* const dst = reinterpret_cast<u32x4*>(A + kA + granule<BN>(id / (BN / 16), id % (BN / 16)));
+                dst[0] = half_out[0];
+                dst[1] = half_out[1];
+            }
         } else {
-            *reinterpret_cast<uint32_t*>(B + packed_at<BN>(l, c >> 2) + 4 * (c & 3)) = vw[n];
+            const int n = i / 4, e = i % 4;
+            uint32_t x = v.a[n][e];
+            if (!ALIGNED) x &= v.left >= 2 * e + 2 ? 0xFFFFFFFFu : (v.left == 2 * e + 1 ? 0xFFFFu : 0u);
+            v.a[n][e] = f32x2_to_bf16x2_rne(__uint_as_float(x << 16) * v.s[2 * e],
+                                            __uint_as_float(x & 0xFFFF0000u) * v.s[2 * e + 1]);
+            if (e == 3) write_a(v, n, A);
         }
+    };
+    auto write_w = [&](const Loads& v, int n, uint8_t* A) {  // MODE 1
+        const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
+        *reinterpret_cast<uint32_t*>(A + kA + packed_at<BN>(l, c >> 2) + 4 * (c & 3)) = v.w[n];
     };
 
     // ---- operands ----
@@ -361,23 +347,35 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
     struct Operands {
-        bf16x8 a[NI];
-        bf16x8 b[MODE == 0 ? NJ : 1];  // MODE 0
-        i32x2 w;                       // MODE 1: byte column of 8 rows
+        bf16x8 a[NI], b[NJ];
+        i32x2 w;  // MODE 1: the byte column that b comes from
     };
-    auto read = [&](const uint8_t* A, int ks, Operands& o) {
+    // Part r of the reads of 16 rows (kReads of them, one LDS instruction each, two for tr16).
+    constexpr int kReads = MODE == 0 ? NI + NJ : NI + 1;
+    auto read = [&](const uint8_t* A, int ks, int r, Operands& o) {
         const uint8_t* const B = A + kA;
         if constexpr (MODE == 0) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) o.b[j] = tr16(B + off_b[j] + ks * 16 * kBRow, 4 * kBRow);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) o.a[i] = tr16(A + off_a[i] + ks * 16 * 2 * BM, 8 * BM);
+            if (r < NJ)
+                o.b[r] = tr16(B + off_b[r] + ks * 16 * kBRow, 4 * kBRow);
+            else
+                o.a[r - NJ] = tr16(A + off_a[r - NJ] + ks * 16 * 2 * BM, 8 * BM);
         } else {
-            o.w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(B + off_b[0] + ks * 16 * kBRow));
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                o.a[i] = *reinterpret_cast<const bf16x8*>(A + off_a[ks] + i * 32 * 2 * BL);
+            if (r == 0)
+                o.w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(B + off_b[0] + ks * 16 * kBRow));
+            else
+                o.a[r - 1] = *reinterpret_cast<const bf16x8*>(A + off_a[ks] + (r - 1) * 32 * 2 * BL);
         }
+    };
+    // MODE 1: four of the eight weights of b[j] (field 2 j + half of the byte column for WN 64,
+    // j for WN 128), the 2 NJ parts of a step's 16 rows.
+    auto expand = [&](Operands& o, int part) {
+        const int j = part >> 1, i = part & 1;
+        const uint32_t hi = __builtin_amdgcn_perm(
+            kHi2w, kHi2w, ((uint32_t)o.w[i] >> (WN == 64 ? 4 * j + 2 * half : 2 * j)) & 0x03030303u);
+        u32x4 x = __builtin_bit_cast(u32x4, o.b[j]);
+        x[2 * i] = __builtin_amdgcn_perm(0u, hi, 0x010C000Cu);
+        x[2 * i + 1] = __builtin_amdgcn_perm(0u, hi, 0x030C020Cu);
+        o.b[j] = __builtin_bit_cast(bf16x8, x);
     };
     f32x16 acc[NI][NJ];
 #pragma unroll
@@ -386,74 +384,95 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    auto multiply = [&](const Operands& o) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            bf16x8 b;
-            if constexpr (MODE == 0)
-                b = o.b[j];
-            else  // field 2 j + half (WN 64) or j (WN 128) of the byte column
-                b = weights_to_bf16(o.w, WN == 64 ? 4 * j + 2 * half : 2 * j);
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.a[i], b, acc[i][j], 0, 0, 0);
-        }
-    };
 
-    // Step it multiplies stage it % 2 while the registers' step it + 1 is converted into the
-    // other stage, spread over all but the last 16 rows' products, and each register is
-    // refilled for step it + 2 as soon as it is free: a load has a whole step to arrive.  One
-    // barrier before the last products of the step, whose operands are already in registers;
-    // the first operands of step it + 1 are read behind it.
-    constexpr int P = KS - 1;  // parts of a conversion
-    auto convert = [&](int part, uint8_t* A) {
-#pragma unroll
-        for (int n = 0; n < NA; ++n)
-            if (n * P / NA == part) store_a(n, A);
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-            if ((NB - 1 - n) * P / NB == part) store_b(n, A + kA);
-    };
-    auto refill = [&](int part) {
-#pragma unroll
-        for (int n = 0; n < NA; ++n)
-            if (n * P / NA == part) load_a(n);
+    // Step it multiplies stage it % 2 while step it + 1, in registers, is converted into the
+    // other stage, and its registers are refilled for step it + 1 + D as soon as they are free.
+    // Vector instructions of a wave wait for its matrix instructions in order, so with both
+    // in runs the SIMD's waves stand behind one unit and then behind the other (measured:
+    // the times of the two added up).  So each product is a slot that also carries a few
+    // vector instructions of the conversion, of the expansion of the next weights, or an
+    // LDS or memory access, and nothing is moved across slots.  One barrier before the last
+    // 16 rows of the step, whose operands are already in registers; the first operands of
+    // step it + 1 are read behind it.
+    constexpr int NM = NI * NJ;
+    constexpr int S = (KS - 1) * NM;  // slots that convert
+    auto convert = [&](Loads& v, int slot, uint8_t* A, bool all) {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
-            if ((NB - 1 - n) * P / NB == part) load_b(n);
-        if (part == P - 1) load_s();
+            if (MODE == 1 && (all || n * S / NB == slot)) {
+                write_w(v, n, A);
+                load_b(v, n);
+            }
+#pragma unroll
+        for (int n = 0; n < NA; ++n)
+            if (MODE == 0 && (all || n * S / NA == slot)) {
+                write_a(v, n, A);
+                load_a(v, n);
+            }
+#pragma unroll
+        for (int i = 0; i < kSlices; ++i)
+            if (all || i * S / kSlices == slot) {
+                convert_slice(v, i, A);
+                if (MODE == 0 && i % 9 == 8) load_b(v, i / 9);
+                if (MODE == 1 && i % 4 == 3) load_a(v, i / 4);
+            }
+        if (all || slot == S - 1) load_s(v);
     };
     auto advance = [&]() {
         s_next += G;
         l0 += G * BL;
         locate();
     };
+    // operands of the 16 rows after the current ones: reads in the first slots, expansion in
+    // the last
+    auto next_operands = [&](const uint8_t* A, int ks, int slot, Operands& o) {
+#pragma unroll
+        for (int r = 0; r < kReads; ++r)
+            if (r * ((NM + 1) / 2) / kReads == slot) read(A, ks, r, o);
+        if (MODE == 1) {
+#pragma unroll
+            for (int e = 0; e < 2 * NJ; ++e)
+                if (NM / 2 + e * (NM - NM / 2) / (2 * NJ) == slot) expand(o, e);
+        }
+    };
     Operands op[2];
     locate();
 #pragma unroll
-    for (int part = 0; part < P; ++part) refill(part);
+    for (int d = 0; d < D; ++d) {
+        if (d > 0) advance();
+#pragma unroll
+        for (int n = 0; n < NA; ++n) load_a(ld[d], n);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) load_b(ld[d], n);
+        load_s(ld[d]);
+    }
     advance();
-#pragma unroll
-    for (int part = 0; part < P; ++part) convert(part, stage);
-#pragma unroll
-    for (int part = 0; part < P; ++part) refill(part);
+    convert(ld[0], 0, stage, true);
     __syncthreads();
-    read(stage, 0, op[0]);
-    for (int it = 0; it < nsteps; ++it) {
-        uint8_t* const cur = stage + (it & 1) * kBuf;
-        uint8_t* const nxt = stage + ((it + 1) & 1) * kBuf;
-        advance();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            if (ks < KS - 1) {
-                read(cur, ks + 1, op[(ks + 1) & 1]);
-                convert(ks, nxt);
-                refill(ks);
-            } else {
-                __syncthreads();
-                read(nxt, 0, op[0]);
+    for (int slot = 0; slot < NM; ++slot) next_operands(stage, 0, slot, op[0]);
+    for (int it0 = 0; it0 < nsteps; it0 += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int it = it0 + d;
+            if (D > 1 && it >= nsteps) break;
+            uint8_t* const cur = stage + (it & 1) * kBuf;
+            uint8_t* const nxt = stage + ((it + 1) & 1) * kBuf;
+            advance();
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const bool last = ks == KS - 1;
+                if (last) __syncthreads();
+                Operands& o = op[ks & 1];
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    acc[m % NI][m / NI] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        o.a[m % NI], o.b[m / NI], acc[m % NI][m / NI], 0, 0, 0);
+                    next_operands(last ? nxt : cur, last ? 0 : ks + 1, m, op[(ks + 1) & 1]);
+                    if (!last) convert(ld[(d + 1) % D], ks * NM + m, nxt, false);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            multiply(op[ks & 1]);
         }
     }
 
@@ -546,6 +565,7 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const float* __restrict_
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
     float4 s = *reinterpret_cast<const float4*>(part + i);
+#pragma unroll 4
     for (int k = 1; k < slices; ++k) {
         const float4 v = *reinterpret_cast<const float4*>(part + k * n + i);
         s.x += v.x;
@@ -565,19 +585,22 @@ struct GradPlan {
     int cfg, slices, steps;
 };
 struct GradCfg {
-    int bm, bn, wm, wn, g, bl;
+    int bm, bn, wm, wn, g, bl, d;
 };
-constexpr GradCfg kCfg[] = {{256, 256, 128, 64, 1, 64},
-                            {256, 128, 128, 64, 2, 32},
-                            {128, 128, 128, 64, 4, 32},
-                            {32, 256, 32, 64, 2, 32}};
+constexpr GradCfg kCfg[] = {
+    {256, 256, 128, 64, 1, 64, 1}, {256, 128, 128, 64, 2, 32, 1}, {128, 128, 128, 64, 4, 32, 1},
+    {32, 256, 32, 64, 2, 32, 1},
+};
+// the [l][column] tiles of MODE 0 are swizzled over 128 columns
+constexpr bool takes(int mode, const GradCfg& k) { return mode == 1 || (k.bm >= 128 && k.bn >= 128); }
+constexpr int kCfgs = sizeof(kCfg) / sizeof(kCfg[0]);
 
 GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
     GradPlan best = {0, 1, 0};
     double best_t = 1e300;
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kCfgs; ++c) {
         const GradCfg& k = kCfg[c];
-        if (mode == 0 && c == 3) continue;
+        if (!takes(mode, k)) continue;
         int64_t steps = 0;
         for (int q = 0; q < groups; ++q) steps += (L[q] + k.bl - 1) / k.bl;
         const int64_t tiles = ((I + k.bm - 1) / k.bm) * ((J + k.bn - 1) / k.bn);
@@ -602,11 +625,18 @@ GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
 template <int MODE, int C>
 void launch_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
     constexpr GradCfg k = kCfg[C];
+    if constexpr (takes(MODE, k)) {
     const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices)), block(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g);
     if (aligned)
-        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, true>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, true>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, false>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, false>), grid, block, 0, stream, a);
+    }
+}
+
+template <int MODE, size_t... C>
+void launch_mode(int cfg, const GradArgs& a, bool aligned, hipStream_t stream, std::index_sequence<C...>) {
+    ((cfg == (int)C ? launch_cfg<MODE, (int)C>(a, aligned, stream) : (void)0), ...);
 }
 
 hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, void* workspace,
@@ -622,16 +652,10 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
     a.steps = pl.steps;
     a.slices = pl.slices;
     a.part = static_cast<float*>(workspace);
-    if (mode == 0) {
-        if (pl.cfg == 0) launch_cfg<0, 0>(a, aligned, stream);
-        else if (pl.cfg == 1) launch_cfg<0, 1>(a, aligned, stream);
-        else launch_cfg<0, 2>(a, aligned, stream);
-    } else {
-        if (pl.cfg == 0) launch_cfg<1, 0>(a, aligned, stream);
-        else if (pl.cfg == 1) launch_cfg<1, 1>(a, aligned, stream);
-        else if (pl.cfg == 2) launch_cfg<1, 2>(a, aligned, stream);
-        else launch_cfg<1, 3>(a, aligned, stream);
-    }
+    if (mode == 0)
+        launch_mode<0>(pl.cfg, a, aligned, stream, std::make_index_sequence<kCfgs>());
+    else
+        launch_mode<1>(pl.cfg, a, aligned, stream, std::make_index_sequence<kCfgs>());
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.slices == 1) return e;
     hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream,
