@@ -71,9 +71,9 @@ struct GradArgs {
     float* part;  // (slices, I, J) when slices > 1
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
-    const int64_t n = bytes < 0 ? 0 : (bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes > 0 ? bytes : 0,
+                                             0x00020000);
 }
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
@@ -163,14 +163,26 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
     const int nsteps = (s1 - s0 + G - 1) / G;
 
     // ---- loads: the step to load next ----
-    int s_next = s0 + g;  // its index; MODE 1: group q, column l0 of it
-    int q = 0, l0 = 0, L = p.L[0], Lpad = (L + BL - 1) / BL * BL;
-    const uint16_t* pa = p.dy[0];
-    const uint8_t* pb = p.b[0];
-    const float* ps = p.scale[0];
+    // Its descriptors move on by scalar adds.  left: rows (MODE 0) or columns (MODE 1) of l from
+    // the step's start to the end of what the block sums of them; at or below zero past the
+    // end, where the descriptors are empty and read as zeros.
+    int left, end;  // MODE 1: end of the block's share, from the start of group q (padded)
+    int l0 = (s0 + g) * BL, q = 0, L = p.L[0];
     const int row_bytes = J / 4;
+    const int rows_a = I - i0 < BM ? I - i0 : BM;  // MODE 1
+    const int step_l = G * BL;
+    const uint8_t *pa, *pb, *ps;
     uint32_t voff_a[NA], voff_b[NB];
-    auto offsets_a = [&]() {
+    auto padded = [](int l) { return (l + BL - 1) / BL * BL; };
+    // the last element of rows at odd places lies in a dword that the descriptor has to cover
+    auto whole = [](int bytes) { return ALIGNED ? bytes : (bytes + 3) & ~3; };
+    auto enter = [&]() {  // at l0 of group q
+        const int stop = L < end ? L : end;
+        left = stop - l0;
+        pa = reinterpret_cast<const uint8_t*>(
+            p.dy[q] + (MODE == 0 ? (int64_t)l0 * I + i0 : (int64_t)i0 * L));
+        pb = p.b[q] + (MODE == 0 ? (int64_t)l0 * J + j0 : (int64_t)l0 * row_bytes + j0 / 4);
+        ps = reinterpret_cast<const uint8_t*>(p.scale[q] + l0);
 #pragma unroll
         for (int n = 0; n < NA; ++n) {
             const int id = tg + n * TG;
@@ -182,51 +194,50 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
                                 : 0x80000000u;
         }
     };
-    offsets_a();
+    end = s1 * BL;
+    if constexpr (MODE == 1) {
+        while (q + 1 < p.groups && l0 >= padded(L)) {
+            l0 -= padded(L);
+            end -= padded(L);
+            L = p.L[++q];
+        }
+    }
+    enter();
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
         voff_b[n] = MODE == 0 ? (uint32_t)(l * J + 16 * c) : (uint32_t)(l * row_bytes + 4 * c);
     }
     __amdgpu_buffer_rsrc_t ra, rb, rs;
-    // the last element of rows at odd places lies in a dword that the descriptor has to cover
-    auto whole = [](int64_t bytes) { return ALIGNED ? bytes : (bytes + 3) & ~(int64_t)3; };
-    // descriptors of the step s_next (empty ones past the end: they read as zeros)
-    auto locate = [&]() {
+    auto describe = [&]() {
+        // sizes of at most 256 rows of 2^20 elements: 32 bits hold them
+        const bool live = left > 0;
+        const int rows = left < BL ? left : BL;
         if constexpr (MODE == 0) {
-            const bool live = s_next < s1;
-            l0 = live ? s_next * BL : 0;
-            const int rows = !live ? 0 : (L - l0 < BL ? L - l0 : BL);
-            ra = rsrc(pa + (int64_t)l0 * I + i0, rows ? whole(((int64_t)rows * I - i0) * 2) : 0);
-            rb = rsrc(pb + (int64_t)l0 * J + j0, rows ? (int64_t)rows * J - j0 : 0);
-            rs = rsrc(ps + l0, (int64_t)rows * 4);
+            ra = rsrc(pa, live ? whole((rows * I - i0) * 2) : 0);
+            rb = rsrc(pb, live ? rows * J - j0 : 0);
         } else {
-            if (l0 >= Lpad) {
-                // past the group's last step: the groups that follow (a dead step stays put)
-                while (q + 1 < p.groups && l0 >= Lpad) {
-                    l0 -= Lpad;
-                    L = p.L[++q];
-                    Lpad = (L + BL - 1) / BL * BL;
-                }
-                pa = p.dy[q];
-                pb = p.b[q];
-                ps = p.scale[q];
-                offsets_a();
-            }
-            const bool live = s_next < s1;
-            const int at = live ? l0 : 0;
-            const int cols = !live ? 0 : (L - at < BL ? L - at : BL);
-            const int rows = I - i0 < BM ? I - i0 : BM;
-            ra = rsrc(pa + (int64_t)i0 * L, live ? whole((int64_t)rows * L * 2) : 0);
-            rb = rsrc(pb + (int64_t)at * row_bytes + j0 / 4,
-                      live ? whole((int64_t)cols * row_bytes - j0 / 4) : 0);
-            rs = rsrc(ps + at, (int64_t)cols * 4);
+            ra = rsrc(pa, live ? whole(rows_a * L * 2) : 0);
+            rb = rsrc(pb, live ? whole(rows * row_bytes - j0 / 4) : 0);
         }
+        rs = rsrc(ps, live ? rows * 4 : 0);
     };
-    if constexpr (MODE == 1) {
-        l0 = s_next * BL;  // s_next counts the padded steps of all groups
-        // locate() walks to the group
-    }
+    auto advance = [&]() {
+        l0 += step_l;
+        left -= step_l;
+        if (MODE == 0) pa += (int64_t)step_l * I * 2;
+        pb += (int64_t)step_l * (MODE == 0 ? J : row_bytes);
+        ps += step_l * 4;
+        if (MODE == 1 && left <= 0 && q + 1 < p.groups && l0 < end) {  // on to the next group
+            while (q + 1 < p.groups && l0 >= padded(L)) {
+                l0 -= padded(L);
+                end -= padded(L);
+                L = p.L[++q];
+            }
+            enter();
+        }
+        describe();
+    };
 
     struct Loads {
         u32x4 a[NA];
@@ -241,7 +252,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
             v.a[n] = ALIGNED ? load16(ra, voff_a[n]) : load8_half(ra, voff_a[n], 0);
         } else {
             if (ALIGNED) {  // whole chunks: those past the row's end read as zeros
-                const bool in = l0 + 8 * (tg % (BL / 8)) < L;
+                const bool in = 8 * (tg % (BL / 8)) < left;
                 v.a[n] = __builtin_bit_cast(
                     u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? voff_a[n] : 0x80000000u, 2 * l0, 0));
             } else {
@@ -270,7 +281,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
                 v.s[e] = __uint_as_float(a0[e]);
                 v.s[4 + e] = __uint_as_float(a1[e]);
             }
-            v.left = L - l0 - 8 * (tg % (BL / 8));
+            v.left = left - 8 * (tg % (BL / 8));
         }
     };
 
@@ -418,11 +429,6 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
             }
         if (all || slot == S - 1) load_s(v);
     };
-    auto advance = [&]() {
-        s_next += G;
-        l0 += G * BL;
-        locate();
-    };
     // operands of the 16 rows after the current ones: reads in the first slots, expansion in
     // the last
     auto next_operands = [&](const uint8_t* A, int ks, int slot, Operands& o) {
@@ -436,7 +442,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
         }
     };
     Operands op[2];
-    locate();
+    describe();
 #pragma unroll
     for (int d = 0; d < D; ++d) {
         if (d > 0) advance();
@@ -451,13 +457,12 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(Gr
     __syncthreads();
 #pragma unroll
     for (int slot = 0; slot < NM; ++slot) next_operands(stage, 0, slot, op[0]);
-    for (int it0 = 0; it0 < nsteps; it0 += D) {
+    for (int it = 0; it < nsteps; it += D) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            const int it = it0 + d;
-            if (D > 1 && it >= nsteps) break;
-            uint8_t* const cur = stage + (it & 1) * kBuf;
-            uint8_t* const nxt = stage + ((it + 1) & 1) * kBuf;
+            if (D > 1 && it + d >= nsteps) break;
+            uint8_t* const cur = stage + ((it + d) & 1) * kBuf;
+            uint8_t* const nxt = stage + ((it + d + 1) & 1) * kBuf;
             advance();
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
