@@ -690,6 +690,10 @@ def swiglu_backward(dh, g, u, g_scale=None, u_scale=None):
     return dg, du
 
 
+# ctypes array types by number of groups (made once: making one costs as much as a call)
+_ARRAYS = [(ctypes.c_void_p * n, ctypes.c_int64 * n) for n in range(1, MAX_GROUPS + 1)]
+
+
 def grad_input_grouped(dy, packed, w_scale, out=None, workspace=None):
     """Gradient of up to MAX_GROUPS products with respect to the input they share, summed:
     dx = sum_g dy_g (w_scale_g * w_g), bf16 (M, K).
@@ -702,14 +706,14 @@ def grad_input_grouped(dy, packed, w_scale, out=None, workspace=None):
     M = _rows(dy[0], "dy[0]")[0]
     K = 4 * _rows(packed[0], "packed[0]")[1]
     d = dy[0].device
-    Ns = [int(_rows(t, f"packed[{g}]")[0]) for g, t in enumerate(packed)]
+    Ns = [_rows(t, "packed")[0] for t in packed]
     if out is None:
         out = torch.empty((M, K), dtype=torch.bfloat16, device=d)
-    ptrs = ctypes.c_void_p * G
-    DY = ptrs(*[_arg(t, torch.bfloat16, f"dy[{g}]", (M, Ns[g]), d) for g, t in enumerate(dy)])
-    P = ptrs(*[_arg(t, torch.uint8, f"packed[{g}]", (Ns[g], K // 4), d) for g, t in enumerate(packed)])
-    S = ptrs(*[_arg(t, torch.float32, f"w_scale[{g}]", (Ns[g],), d) for g, t in enumerate(w_scale)])
-    NN = (ctypes.c_int64 * G)(*Ns)
+    ptrs, sizes = _ARRAYS[G - 1] if G <= MAX_GROUPS else (ctypes.c_void_p * G, ctypes.c_int64 * G)
+    DY = ptrs(*[_arg(t, torch.bfloat16, "dy", (M, n), d) for t, n in zip(dy, Ns)])
+    P = ptrs(*[_arg(t, torch.uint8, "packed", (n, K // 4), d) for t, n in zip(packed, Ns)])
+    S = ptrs(*[_arg(t, torch.float32, "w_scale", (n,), d) for t, n in zip(w_scale, Ns)])
+    NN = sizes(*Ns)
     need = int(lib().bitnet_grad_input_workspace_size(M, K, G, NN)) if workspace is None else 0
     ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
     _run("bitnet_grad_input", d, M, K, G, DY, P, S, NN, _arg(out, torch.bfloat16, "out", (M, K), d),

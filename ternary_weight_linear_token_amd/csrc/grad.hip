@@ -19,23 +19,29 @@
 // output below that.
 //
 // Design:
-//  * v_mfma_f32_32x32x16_bf16.  A wave owns WM x 64 outputs; 128 x 64 needs 12 KB of LDS
-//    reads per 32 l against 16 KB of 64 x 64 twice over, and the LDS read rate is what a
-//    64 x 64 wave tile would be bound by.  8 waves per block: (BM / WM) x (BN / 64) waves
-//    for each of G groups; group g takes every G-th step of l, and the groups' sums are
-//    joined through LDS at the end, so that small outputs keep large wave tiles.
-//  * Operands whose contraction index is the slow one in memory (B always, A in MODE 0) lie
-//    in LDS as [l][column] and are read with the transposing ds_read_b64_tr_b16: a group of
-//    16 lanes reads 4 rows of 16 columns and lane t gets column t of the 4 rows.  The 32-byte
-//    granules of row l are XORed with 2 (l & 3), so the four rows of a read fall in
-//    different banks.
-//  * Loads go through registers (B is expanded on the way): step t + 1 is loaded while step t
-//    is multiplied, then converted and written to the other LDS buffer; one barrier a step.
+//  * v_mfma_f32_32x32x16_bf16; a wave owns WM x WN outputs, (BM / WM) x (BN / WN) waves make a
+//    group, and G groups share a tile: group g takes every G-th step of BL values of l, and
+//    the groups' sums are joined through LDS at the end (in halves, a fixed order), so that
+//    small outputs keep the chip busy with large wave tiles.
+//  * Operands whose contraction index is the slow one in memory lie in LDS as [l][column] and
+//    are read transposed: bf16 rows (MODE 0) with ds_read_b64_tr_b16 (a group of 16 lanes reads
+//    4 rows of 16 columns, lane t gets column t), packed weights (MODE 1) as they are, 2 bits
+//    each, with ds_read_b64_tr_b8 (8 rows of 16 bytes, lane t gets byte column t: four weights
+//    of each of 8 rows), expanded in registers by byte lookups.  Rows are XOR-swizzled so that
+//    the rows of a read fall in different banks.
+//  * Loads go through registers, since one operand is converted on the way.  Every matrix
+//    instruction is a slot that also carries its share of the conversion (see the main loop);
+//    descriptors move on by scalar adds, because the instruction issue of a wave counts: 129
+//    scalar instructions a step cost 8% at 8192^3.
 //  * Few output tiles: l is also split over blocks (slices); every slice writes fp32 partial
 //    sums to the workspace and a second launch adds them in a fixed order.
 //  * Tails: rows past the end of l read as zeros through the buffer descriptors' bounds or a
-//    mask; rows that start off a dword are put together from the dwords around them; columns past i or j are computed from whatever lies there and never stored (they
-//    only reach their own outputs).
+//    mask; rows that start off a dword are put together from the dwords around them; columns
+//    past i or j are computed from whatever lies there and never stored (they only reach
+//    their own outputs).
+// Measured (dx and dw, bf16 out): 8192^3 1334 and 1150 TFLOP/s (a library bf16 product of that
+// size: 1264), the matrix cores busy half of the time.
+#include <cmath>
 #include <utility>
 
 #include "device_common.hpp"
@@ -110,8 +116,8 @@ __device__ __forceinline__ int chunk(int i, int c) {
     return i * (2 * BL) + ((c ^ (CPR == 8 ? (i & 7) : ((i >> 1) & 3))) << 4);
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, int D, bool ALIGNED>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G) void grad_kernel(GradArgs p) {
+template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, int D, int W, bool ALIGNED>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel(GradArgs p) {
     constexpr int WPG = (BM / WM) * (BN / WN);  // waves of a group
     constexpr int TG = 64 * WPG;                // threads of a group
     constexpr int NI = WM / 32, NJ = WN / 32, KS = BL / 16;
@@ -589,35 +595,57 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const float* __restrict_
 struct GradPlan {
     int cfg, slices, steps;
 };
+// A tile configuration and what it costs: d steps of loads in flight, at least w waves per
+// SIMD (4: at most 128 registers), blocks per CU, and the microseconds of a block's
+// prologue and epilogue and of a step of a group, alone on its CU and among `blocks` of them
+// (measured at 512 to 2048 tokens on 2B and 8B layers; full chip, so at its clocks).
 struct GradCfg {
-    int bm, bn, wm, wn, g, bl, d;
+    int mode, bm, bn, wm, wn, g, bl, d, w, blocks;
+    double base, step_alone, step_full;
 };
 constexpr GradCfg kCfg[] = {
-    {256, 256, 128, 64, 1, 64, 1}, {256, 128, 128, 64, 2, 32, 1}, {128, 128, 128, 64, 4, 32, 1},
-    {32, 256, 32, 64, 2, 32, 1},
+    // weight gradient.  256 x 256 is the fastest per flop (2048 x 4096 x 14336: 262 us, 128 x 128
+    // tiles 305); its 256 blocks at a time leave most of the chip idle in a short last round
+    // (512 x 6912 x 2560, 270 tiles: 53 us), which 128 x 128 tiles, two or four blocks per CU,
+    // fill better (45 and 43 us); four share a CU only at half the rows per step.
+    {0, 256, 256, 128, 64, 1, 64, 1, 1, 1, 13, 1.8, 1.8},
+    {0, 128, 128, 64, 64, 1, 64, 1, 1, 2, 8, 0.73, 1.15},
+    {0, 128, 128, 64, 64, 1, 32, 1, 4, 4, 8, 0.43, 1.25},
+    // input gradient.  256 x 256 for the largest (2048 x 28672 x 4096: 406 us, 256 x 128 519);
+    // 256 x 128 where that makes one round of the chip (2048 x 4096 x 4096: 75 us against 78);
+    // 64 x 128 with the sum over four groups of waves for hundreds of tokens (512 x 3840 x 2560:
+    // 26 us, 128 x 128 in three slices 29); 32 x 128 below (4 x 2560 x 2560 in slices: 9.5 us).
+    {1, 256, 256, 128, 64, 1, 64, 1, 1, 1, 8, 1.7, 1.7},
+    {1, 256, 128, 128, 64, 2, 32, 1, 1, 1, 9, 1.0, 1.0},
+    {1, 64, 128, 64, 64, 4, 32, 2, 1, 1, 7, 0.59, 0.59},
+    {1, 32, 128, 32, 64, 4, 32, 2, 1, 2, 6, 0.45, 0.67},
 };
-// the [l][column] tiles of MODE 0 are swizzled over 128 columns
-constexpr bool takes(int mode, const GradCfg& k) { return mode == 1 || (k.bm >= 128 && k.bn >= 128); }
 constexpr int kCfgs = sizeof(kCfg) / sizeof(kCfg[0]);
+constexpr int kCUs = 256;
 
+// The configuration and number of slices with the least estimated time.
 GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
     GradPlan best = {0, 1, 0};
     double best_t = 1e300;
     for (int c = 0; c < kCfgs; ++c) {
         const GradCfg& k = kCfg[c];
-        if (!takes(mode, k)) continue;
+        if (k.mode != mode) continue;
         int64_t steps = 0;
         for (int q = 0; q < groups; ++q) steps += (L[q] + k.bl - 1) / k.bl;
         const int64_t tiles = ((I + k.bm - 1) / k.bm) * ((J + k.bn - 1) / k.bn);
-        for (int64_t s = 1; s <= 32; ++s) {
+        for (int64_t s = 1; s <= 16; ++s) {
+            // at least two steps per group of a slice, at most 64 MB of partial sums
             if (s > 1 && (steps < 2 * s * k.g || s * I * J * 4 > ((int64_t)64 << 20))) break;
-            const int64_t rounds = (tiles * s + 255) / 256;
-            const int64_t per = ((steps + s - 1) / s + k.g - 1) / k.g;  // steps of a group
-            // a step costs its matrix products (8 waves at about half of the peak rate) or a
-            // fixed latency; a block its prologue and epilogue; a join its bytes
-            const double step_us = 0.45 * k.bl / 32.0 * (k.wm / 128.0) + 0.35;
-            const double t = rounds * (per * step_us + 3.0 + k.wm / 64.0) +
-                             (s > 1 ? 3.0 + (s + 1) * I * J * 4.0 / 3e6 : 0.0);
+            const double per = (double)(((steps + s - 1) / s + k.g - 1) / k.g);
+            const double x = (double)(tiles * s) / (kCUs * k.blocks);
+            double t;
+            if (tiles * s <= kCUs)
+                t = k.base + per * k.step_alone;
+            else if (x <= 1)
+                t = k.base + per * k.step_full;
+            else  // blocks of a CU do not end together: half of a last round's raggedness
+                t = (k.blocks > 1 ? 0.5 * (x + std::ceil(x)) : std::ceil(x)) * (k.base + per * k.step_full);
+            if (s > 1) t += 3.0 + (s + 1) * I * J * 4.0 / 5e6;  // the join: a launch, its bytes
             if (t < best_t) {
                 best_t = t;
                 best = {c, (int)s, (int)steps};
@@ -627,21 +655,22 @@ GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
     return best;
 }
 
-template <int MODE, int C>
+template <int C>
 void launch_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
     constexpr GradCfg k = kCfg[C];
-    if constexpr (takes(MODE, k)) {
-    const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices)), block(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g);
+    const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices));
+    const dim3 block(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g);
     if (aligned)
-        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, true>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, true>), grid,
+                           block, 0, stream, a);
     else
-        hipLaunchKernelGGL((grad_kernel<MODE, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, false>), grid, block, 0, stream, a);
-    }
+        hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, false>), grid,
+                           block, 0, stream, a);
 }
 
-template <int MODE, size_t... C>
-void launch_mode(int cfg, const GradArgs& a, bool aligned, hipStream_t stream, std::index_sequence<C...>) {
-    ((cfg == (int)C ? launch_cfg<MODE, (int)C>(a, aligned, stream) : (void)0), ...);
+template <size_t... C>
+void launch_any(int cfg, const GradArgs& a, bool aligned, hipStream_t stream, std::index_sequence<C...>) {
+    ((cfg == (int)C ? launch_cfg<(int)C>(a, aligned, stream) : (void)0), ...);
 }
 
 hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, void* workspace,
@@ -657,10 +686,7 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
     a.steps = pl.steps;
     a.slices = pl.slices;
     a.part = static_cast<float*>(workspace);
-    if (mode == 0)
-        launch_mode<0>(pl.cfg, a, aligned, stream, std::make_index_sequence<kCfgs>());
-    else
-        launch_mode<1>(pl.cfg, a, aligned, stream, std::make_index_sequence<kCfgs>());
+    launch_any(pl.cfg, a, aligned, stream, std::make_index_sequence<kCfgs>());
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.slices == 1) return e;
     hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream,

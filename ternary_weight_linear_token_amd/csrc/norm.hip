@@ -226,9 +226,12 @@ __device__ __forceinline__ void x_to_f32(const XVec<V, CODES>& v, float inv, flo
 
 // Blocks of TEAMS teams; the teams of a block walk the rows in step (every wave reaches
 // every barrier; a team past the last row works on zeros).
-template <int V, int WPR, bool CODES>
+// A lane holds one group of V columns where 16 waves cover the row so: with two, the column
+// sums, the weight and two rows in flight take 146 registers and one block fills a CU
+// (8192 x 4096 from the checkpoint: 50 us against 43).
+template <int V, int WPR, int G, bool CODES>
 __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void layernorm_back_kernel(NormBackArgs p) {
-    constexpr int G = kTeamGroups, kStride = 64 * WPR, TEAMS = WPR == 16 ? 1 : 8 / WPR;
+    constexpr int kStride = 64 * WPR, TEAMS = WPR == 16 ? 1 : 8 / WPR;
     __shared__ float s_red[2][TEAMS][WPR][2];
     __shared__ float s_join[TEAMS > 1 ? kStride * G * V : 1];
     const int team = threadIdx.x / kStride, lr = threadIdx.x % kStride;
@@ -418,24 +421,38 @@ __global__ __launch_bounds__(256) void layernorm_cols_kernel(NormBackArgs p) {
     part[p.K + k] = db;
 }
 
-// out[k] = sum_b part[b][which][k]: 32 columns per block, eight threads per column, their
-// sums added in order.
-__global__ __launch_bounds__(256) void layernorm_join_kernel(const float* __restrict__ part, int blocks,
-                                                             int64_t K, float* dweight, float* dbias) {
-    __shared__ float s[8][33];
-    const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-    const int64_t k = (int64_t)blockIdx.x * 32 + c;
+// out[k] = sum_b part[b][which][k]: 64 columns per block, 64 rows of 16 threads that each add
+// every 64th partial of four columns, then the 64 sums of a column in order.
+__global__ __launch_bounds__(1024) void layernorm_join_kernel(const float* __restrict__ part, int blocks,
+                                                              int64_t K, float* dweight, float* dbias) {
+    __shared__ float s[64][68];
+    const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+    const int64_t k = (int64_t)blockIdx.x * 64 + 4 * c;
     float* const out = blockIdx.y ? dbias : dweight;
     if (!out) return;
-    float sum = 0.0f;
-    if (k < K)
-        for (int b = r; b < blocks; b += 8) sum += part[((int64_t)b * 2 + blockIdx.y) * K + k];
-    s[r][c] = sum;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (k < K) {
+#pragma unroll 4
+        for (int b = r; b < blocks; b += 64) {
+            const float4 v = *reinterpret_cast<const float4*>(part + ((int64_t)b * 2 + blockIdx.y) * K + k);
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+        }
+    }
+    *reinterpret_cast<float4*>(&s[r][4 * c]) = sum;
     __syncthreads();
-    if (r == 0 && k < K) {
+    const int col = threadIdx.x & 63, q = threadIdx.x >> 6;  // 16 waves, four sums each
+    float t = (s[4 * q][col] + s[4 * q + 1][col]) + (s[4 * q + 2][col] + s[4 * q + 3][col]);
+    __syncthreads();
+    s[q][col] = t;
+    __syncthreads();
+    const int64_t kc = (int64_t)blockIdx.x * 64 + col;
+    if (q == 0 && kc < K) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) sum += s[i][c];
-        out[k] = sum;
+        for (int i = 1; i < 16; ++i) t += s[i][col];
+        out[kc] = t;
     }
 }
 
@@ -464,9 +481,16 @@ int team_waves(int64_t K, int V) {
     return 0;
 }
 
+// Waves per row of the backward pass, one group a lane up to 16 waves, then two; 0: too long.
+int back_waves(int64_t K, int V) {
+    for (int w = 1; w <= 16; w *= 2)
+        if (K <= (int64_t)w * 64 * V) return w;
+    return K <= (int64_t)16 * 64 * 2 * V ? 16 : 0;
+}
+
 // Blocks of the backward pass.
 int64_t back_blocks(int64_t M, int64_t K) {
-    const int w = team_waves(K, K % 8 == 0 ? 8 : 4);
+    const int w = back_waves(K, K % 8 == 0 ? 8 : 4);
     if (w == 0) return M < 64 * 32 ? (M + 31) / 32 : 64;
     const int64_t teams = w == 16 ? 1 : 8 / w;
     const int64_t b = (M + 2 * teams - 1) / (2 * teams);
@@ -501,21 +525,24 @@ hipError_t launch_layernorm_v(const NormArgs& a, hipStream_t stream) {
 template <int V, bool CODES>
 hipError_t launch_back_v(const NormBackArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)back_blocks(a.M, a.K));
-    switch (team_waves(a.K, V)) {
+    switch (back_waves(a.K, V)) {
         case 1:
-            hipLaunchKernelGGL((layernorm_back_kernel<V, 1, CODES>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 1, 1, CODES>), grid, dim3(512), 0, stream, a);
             break;
         case 2:
-            hipLaunchKernelGGL((layernorm_back_kernel<V, 2, CODES>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 2, 1, CODES>), grid, dim3(512), 0, stream, a);
             break;
         case 4:
-            hipLaunchKernelGGL((layernorm_back_kernel<V, 4, CODES>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 4, 1, CODES>), grid, dim3(512), 0, stream, a);
             break;
         case 8:
-            hipLaunchKernelGGL((layernorm_back_kernel<V, 8, CODES>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((layernorm_back_kernel<V, 8, 1, CODES>), grid, dim3(512), 0, stream, a);
             break;
         case 16:
-            hipLaunchKernelGGL((layernorm_back_kernel<V, 16, CODES>), grid, dim3(1024), 0, stream, a);
+            if (a.K <= (int64_t)16 * 64 * V)
+                hipLaunchKernelGGL((layernorm_back_kernel<V, 16, 1, CODES>), grid, dim3(1024), 0, stream, a);
+            else
+                hipLaunchKernelGGL((layernorm_back_kernel<V, 16, 2, CODES>), grid, dim3(1024), 0, stream, a);
             break;
         default: {
             const unsigned rows = (unsigned)(a.M < 1024 ? a.M : 1024);
@@ -557,7 +584,7 @@ hipError_t launch_layernorm_back(const uint16_t* dy, const void* x, const float*
         if (e != hipSuccess) return e;
     }
     if (!sums) return hipSuccess;
-    hipLaunchKernelGGL(layernorm_join_kernel, dim3((unsigned)((K + 31) / 32), 2), dim3(256), 0, stream,
+    hipLaunchKernelGGL(layernorm_join_kernel, dim3((unsigned)((K + 63) / 64), 2), dim3(1024), 0, stream,
                        static_cast<const float*>(workspace), M > 0 ? (int)back_blocks(M, K) : 0, K, dweight,
                        dbias);
     return hipGetLastError();
