@@ -556,9 +556,9 @@ def quant_act_pow2(x, xq=None, a_scale=None):
     M, K = _rows(x, "x")
     d = x.device
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=d)
+        xq = torch.empty_like(x, dtype=torch.int8)
     if a_scale is None:
-        a_scale = torch.empty((M,), dtype=torch.float32, device=d)
+        a_scale = x.new_empty(M, dtype=torch.float32)
     _run("bitnet_quant_act_pow2", d, _arg(x, torch.bfloat16, "x", (M, K), d), M, K,
          _arg(xq, torch.int8, "xq", (M, K), d), _arg(a_scale, torch.float32, "a_scale", (M,), d))
     return xq, a_scale
@@ -569,7 +569,7 @@ def dequant_act(xq, a_scale, out=None):
     M, K = _rows(xq, "xq")
     d = xq.device
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=d)
+        out = torch.empty_like(xq, dtype=torch.bfloat16)
     _run("bitnet_dequant_act", d, _arg(xq, torch.int8, "xq", (M, K), d),
          _arg(a_scale, torch.float32, "a_scale", (M,), d), M, K,
          _arg(out, torch.bfloat16, "out", (M, K), d))
@@ -581,13 +581,13 @@ def _layernorm(x, weight, bias, eps, want_y, scale, return_stats, out=None):
     d = x.device
     y, xq, a_scale, mean, rstd = out, None, None, None, None
     if want_y and y is None:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=d)
+        y = torch.empty_like(x)
     if scale is not None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=d)
-        a_scale = torch.empty((M,), dtype=torch.float32, device=d)
+        xq = torch.empty_like(x, dtype=torch.int8)
+        a_scale = x.new_empty(M, dtype=torch.float32)
     if return_stats:
-        mean = torch.empty((M,), dtype=torch.float32, device=d)
-        rstd = torch.empty((M,), dtype=torch.float32, device=d)
+        mean = x.new_empty(M, dtype=torch.float32)
+        rstd = x.new_empty(M, dtype=torch.float32)
     ptr = lambda t: None if t is None else t.data_ptr()  # our own allocations
     _run("bitnet_layernorm", d, _arg(x, torch.bfloat16, "x", (M, K), d),
          _arg(weight, torch.float32, "weight", (K,), d), _arg(bias, torch.float32, "bias", (K,), d),
@@ -620,12 +620,12 @@ def layernorm_backward(dy, x, weight, mean, rstd, x_scale=None, need_sums=True, 
     (allocated by default)."""
     M, K = _rows(dy, "dy")
     d = dy.device
-    dx = torch.empty((M, K), dtype=torch.bfloat16, device=d)
+    dx = torch.empty_like(dy)
     dweight = dbias = None
     ws_ptr, ws_bytes, ws = None, 0, None
     if need_sums:
-        dweight = torch.empty((K,), dtype=torch.float32, device=d)
-        dbias = torch.empty((K,), dtype=torch.float32, device=d)
+        dweight = dy.new_empty(K, dtype=torch.float32)
+        dbias = dy.new_empty(K, dtype=torch.float32)
         need = int(lib().bitnet_layernorm_backward_workspace_size(M, K))
         ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
     _run("bitnet_layernorm_backward", d, _arg(dy, torch.bfloat16, "dy", (M, K), d),
@@ -641,12 +641,12 @@ def layernorm_backward(dy, x, weight, mean, rstd, x_scale=None, need_sums=True, 
 def _swiglu(g, u, want_h, scale, checkpoint, out=None):
     M, N = _rows(g, "g")
     d = g.device
-    i8 = lambda: torch.empty((M, N), dtype=torch.int8, device=d)
-    f32 = lambda: torch.empty((M,), dtype=torch.float32, device=d)
+    i8 = lambda: torch.empty_like(g, dtype=torch.int8)
+    f32 = lambda: g.new_empty(M, dtype=torch.float32)
     ptr = lambda t: None if t is None else t.data_ptr()  # our own allocations
     h, hq, hs, ckpt = out, None, None, None
     if want_h and h is None:
-        h = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+        h = torch.empty_like(g)
     if scale is not None:
         hq, hs = i8(), f32()
     if checkpoint:
@@ -681,8 +681,7 @@ def swiglu_backward(dh, g, u, g_scale=None, u_scale=None):
     if (g_scale is None) != (u_scale is None):
         raise ValueError("g_scale and u_scale go together")
     dt = torch.bfloat16 if g_scale is None else torch.int8
-    dg = torch.empty((M, N), dtype=torch.bfloat16, device=d)
-    du = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+    dg, du = torch.empty_like(dh), torch.empty_like(dh)
     _run("bitnet_swiglu_backward", d, _arg(dh, torch.bfloat16, "dh", (M, N), d),
          _arg(g, dt, "g", (M, N), d), _arg(g_scale, torch.float32, "g_scale", (M,), d),
          _arg(u, dt, "u", (M, N), d), _arg(u_scale, torch.float32, "u_scale", (M,), d), M, N,

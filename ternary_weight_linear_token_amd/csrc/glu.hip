@@ -70,9 +70,9 @@ __global__ __launch_bounds__(64 * WPR) void swiglu_kernel(GluArgs p) {
                 const int64_t q = threadIdx.x + (int64_t)i * kStride;
                 h[i] = swiglu_vec<V>(g[i], u[i]);
                 if (p.h && q < groups) store_row_vec<V>(p.h + row, q, h[i]);
-                mg = max_bits<V>(g[i], mg);
-                mu = max_bits<V>(u[i], mu);
-                mh = max_bits<V>(h[i], mh);
+                mg = max_pairs<V>(g[i], mg);
+                mu = max_pairs<V>(u[i], mu);
+                mh = max_pairs<V>(h[i], mh);
             }
         } else {
             for (int64_t q = threadIdx.x; q < groups; q += kStride) {
@@ -80,15 +80,15 @@ __global__ __launch_bounds__(64 * WPR) void swiglu_kernel(GluArgs p) {
                 u[0] = load_row_vec<V>(p.u + row, q);
                 h[0] = swiglu_vec<V>(g[0], u[0]);
                 if (p.h) store_row_vec<V>(p.h + row, q, h[0]);
-                mg = max_bits<V>(g[0], mg);
-                mu = max_bits<V>(u[0], mu);
-                mh = max_bits<V>(h[0], mh);
+                mg = max_pairs<V>(g[0], mg);
+                mu = max_pairs<V>(u[0], mu);
+                mh = max_pairs<V>(h[0], mh);
             }
         }
         if (!codes) continue;
-        mg = wave_max_u32(mg);
-        mu = wave_max_u32(mu);
-        mh = wave_max_u32(mh);
+        mg = wave_max_u32(max_of_pair(mg));
+        mu = wave_max_u32(max_of_pair(mu));
+        mh = wave_max_u32(max_of_pair(mh));
         if (WPR > 1) {
             // the slots of row m are written again two rows later, behind the next row's barrier
             uint32_t(&s)[WPR][3] = s_max[parity];
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void swiglu_back_kernel(GluBackArgs p) {
         for (int e = 0; e < 2; ++e) {
             const int k = 2 * j + e;
             const float s = sigmoid(g[k]);
-            dg[e] = d[k] * u[k] * (s * (1.0f + g[k] * (1.0f - s)));
+            dg[e] = d[k] * u[k] * (s * __builtin_fmaf(g[k], 1.0f - s, 1.0f));
             du[e] = d[k] * (g[k] * s);
         }
         a.w[j] = f32x2_to_bf16x2_rne(dg[0], dg[1]);

@@ -90,8 +90,8 @@ __global__ __launch_bounds__(64 * WPR) void layernorm_kernel(NormArgs p) {
         for (int i = 0; i < G; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                x[i][j] = in[i] ? x[i][j] - mean : 0.0f;
-                sq += x[i][j] * x[i][j];
+                x[i][j] -= mean;
+                if (in[i]) sq = __builtin_fmaf(x[i][j], x[i][j], sq);
             }
         const float rstd = 1.0f / sqrtf(team_sum<WPR>(sq, s_red[1]) / K + p.eps);
         uint32_t mx = 0;
@@ -99,11 +99,12 @@ __global__ __launch_bounds__(64 * WPR) void layernorm_kernel(NormArgs p) {
         for (int i = 0; i < G; ++i) {
 #pragma unroll
             for (int j = 0; j < V / 2; ++j)
-                cur[i].w[j] = f32x2_to_bf16x2_rne(x[i][2 * j] * rstd * w[i][2 * j] + b[i][2 * j],
-                                                  x[i][2 * j + 1] * rstd * w[i][2 * j + 1] + b[i][2 * j + 1]);
+                cur[i].w[j] =
+                    f32x2_to_bf16x2_rne(__builtin_fmaf(x[i][2 * j] * rstd, w[i][2 * j], b[i][2 * j]),
+                                        __builtin_fmaf(x[i][2 * j + 1] * rstd, w[i][2 * j + 1], b[i][2 * j + 1]));
             if (in[i]) {
                 if (p.y) store_row_vec<V>(p.y + m * p.K, threadIdx.x + (int64_t)i * kStride, cur[i]);
-                mx = max_bits<V>(cur[i], mx);
+                mx = max_pairs<V>(cur[i], mx);
             }
         }
         if (threadIdx.x == 0) {
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(64 * WPR) void layernorm_kernel(NormArgs p) {
             if (p.rstd) p.rstd[m] = rstd;
         }
         if (p.xq) {
-            const float a = scale_of(team_max<WPR>(mx, s_max), p.pow2);
+            const float a = scale_of(team_max<WPR>(max_of_pair(mx), s_max), p.pow2);
             if (threadIdx.x == 0) p.a_scale[m] = a;
 #pragma unroll
             for (int i = 0; i < G; ++i)
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(NormArgs p) {
         for (int64_t g = threadIdx.x; g < groups; g += 1024) {
             to_f32<V>(load_row_vec<V>(row, g), x);
 #pragma unroll
-            for (int j = 0; j < V; ++j) sq += (x[j] - mean) * (x[j] - mean);
+            for (int j = 0; j < V; ++j) sq = __builtin_fmaf(x[j] - mean, x[j] - mean, sq);
         }
         const float rstd = 1.0f / sqrtf(team_sum<WPR>(sq, s_red[1]) / K + p.eps);
         auto output = [&](int64_t g) {
@@ -154,22 +155,23 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(NormArgs p) {
             RowVec<V> y;
 #pragma unroll
             for (int j = 0; j < V / 2; ++j)
-                y.w[j] = f32x2_to_bf16x2_rne((x[2 * j] - mean) * rstd * w[2 * j] + b[2 * j],
-                                             (x[2 * j + 1] - mean) * rstd * w[2 * j + 1] + b[2 * j + 1]);
+                y.w[j] = f32x2_to_bf16x2_rne(
+                    __builtin_fmaf((x[2 * j] - mean) * rstd, w[2 * j], b[2 * j]),
+                    __builtin_fmaf((x[2 * j + 1] - mean) * rstd, w[2 * j + 1], b[2 * j + 1]));
             return y;
         };
         uint32_t mx = 0;
         for (int64_t g = threadIdx.x; g < groups; g += 1024) {
             const RowVec<V> y = output(g);
             if (p.y) store_row_vec<V>(p.y + m * p.K, g, y);
-            mx = max_bits<V>(y, mx);
+            mx = max_pairs<V>(y, mx);
         }
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[m] = mean;
             if (p.rstd) p.rstd[m] = rstd;
         }
         if (p.xq) {
-            const float a = scale_of(team_max<WPR>(mx, s_max), p.pow2);
+            const float a = scale_of(team_max<WPR>(max_of_pair(mx), s_max), p.pow2);
             if (threadIdx.x == 0) p.a_scale[m] = a;
             for (int64_t g = threadIdx.x; g < groups; g += 1024)
                 store_codes<V>(p.xq + m * p.K, g, output(g), a);
@@ -287,11 +289,11 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void layernorm_back_kernel(
             for (int j = 0; j < V; ++j) {
                 // columns past the row have dy = 0 and add nothing below
                 xh[i][j] = (xh[i][j] - cur.mean) * cur.rstd;
-                dw[i][j] += d[j] * xh[i][j];
+                dw[i][j] = __builtin_fmaf(d[j], xh[i][j], dw[i][j]);
                 db[i][j] += d[j];
                 g[i][j] = d[j] * w[i][j];
                 s1 += g[i][j];
-                s2 += g[i][j] * xh[i][j];
+                s2 = __builtin_fmaf(g[i][j], xh[i][j], s2);
             }
         }
         s1 = wave_sum_f32(s1);
@@ -317,8 +319,9 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void layernorm_back_kernel(
                 RowVec<V> o;
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j)
-                    o.w[j] = f32x2_to_bf16x2_rne(cur.rstd * (g[i][2 * j] - c1 - xh[i][2 * j] * c2),
-                                                 cur.rstd * (g[i][2 * j + 1] - c1 - xh[i][2 * j + 1] * c2));
+                    o.w[j] = f32x2_to_bf16x2_rne(
+                        cur.rstd * __builtin_fmaf(-c2, xh[i][2 * j], g[i][2 * j] - c1),
+                        cur.rstd * __builtin_fmaf(-c2, xh[i][2 * j + 1], g[i][2 * j + 1] - c1));
                 if (in[i]) store_row_vec<V>(p.dx + m * p.K, lr + (int64_t)i * kStride, o);
             }
         }

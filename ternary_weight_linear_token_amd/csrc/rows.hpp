@@ -50,16 +50,18 @@ __device__ __forceinline__ void to_f32(const RowVec<V>& v, float (&f)[V]) {
         f[2 * i + 1] = __uint_as_float(v.w[i] & 0xFFFF0000u);
     }
 }
-// Running max of |x| as bf16 magnitude bits (monotone for finite values).
+// Running max of |x| as bf16 magnitude bits (monotone for finite values), one in each half of
+// the word: one packed 16-bit max per two values.
 template <int V>
-__device__ __forceinline__ uint32_t max_bits(const RowVec<V>& v, uint32_t mx) {
+__device__ __forceinline__ uint32_t max_pairs(const RowVec<V>& v, uint32_t mx) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = __builtin_bit_cast(u16x2, mx);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        const uint32_t a = v.w[i] & 0x7FFF7FFFu;
-        mx = max(mx, max(a & 0xFFFFu, a >> 16));
-    }
-    return mx;
+    for (int i = 0; i < V / 2; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v.w[i] & 0x7FFF7FFFu));
+    return __builtin_bit_cast(uint32_t, m);
 }
+__device__ __forceinline__ uint32_t max_of_pair(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
 
 __device__ __forceinline__ float wave_sum_f32(float v) {
     return __uint_as_float(wave_reduce_dpp(__float_as_uint(v), [](uint32_t a, uint32_t b) {
@@ -113,20 +115,21 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits, bool pow2) {
     return 127.0f / amax;
 }
 
-// clamp(rne(x * a), -127, 127) of V elements
+// rne(x * a) of V elements as int8: adding 1.5 * 2^23 to fl(x * a) rounds it to an integer,
+// ties to even, and the sum's low byte is that integer.  The clamp to +-127 never binds:
+// |fl(x * a)| <= 127 (1 + 2^-23) < 127.5 for both kinds of scale.
 template <int V>
 __device__ __forceinline__ void store_codes(int8_t* row, int64_t g, const RowVec<V>& v, float a) {
+    constexpr float kMagic = 12582912.0f;
     float f[V];
     to_f32<V>(v, f);
     uint32_t p[V / 4];
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
-        p[i] = 0;
+        uint32_t q[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float r = fminf(fmaxf(rintf(f[4 * i + j] * a), -127.0f), 127.0f);
-            p[i] |= ((uint32_t)(int)r & 0xFFu) << (8 * j);
-        }
+        for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(f[4 * i + j] * a + kMagic);
+        p[i] = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400u) | __builtin_amdgcn_perm(q[3], q[2], 0x04000c0cu);
     }
     if constexpr (V == 8)
         reinterpret_cast<uint2*>(row)[g] = make_uint2(p[0], p[1]);
