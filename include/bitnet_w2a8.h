@@ -391,8 +391,8 @@ int bitnet_quant_act_pow2(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, f
                           void* stream);
 
 /*
- * bitnet_dequant_act -- the values that codes stand for, x[m,k] = bf16(xq[m,k] / a_scale[m])
- * (one fp32 division and one rounding; exact for power-of-two scales).
+ * bitnet_dequant_act -- the values that codes stand for, x[m,k] = bf16(xq[m,k] * (1 / a_scale[m]))
+ * (the reciprocal and the product in fp32; exact for power-of-two scales).
  */
 int bitnet_dequant_act(const int8_t* xq, const float* a_scale, int64_t M, int64_t K, uint16_t* x,
                        void* stream);

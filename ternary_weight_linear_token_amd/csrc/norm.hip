@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * WPR) void layernorm_kernel(NormArgs p) {
     __shared__ float s_red[2][WPR];
     __shared__ uint32_t s_max[WPR];
     const int64_t groups = p.K / V;
-    const float K = (float)p.K;
+    const float inv_k = 1.0f / (float)p.K;
     float w[G][V], b[G][V];
     bool in[G];
 #pragma unroll
@@ -84,16 +84,18 @@ __global__ __launch_bounds__(64 * WPR) void layernorm_kernel(NormArgs p) {
 #pragma unroll
             for (int j = 0; j < V; ++j) sum += x[i][j];
         }
-        const float mean = team_sum<WPR>(sum, s_red[0]) / K;
+        const float mean = team_sum<WPR>(sum, s_red[0]) * inv_k;
         float sq = 0.0f;
 #pragma unroll
         for (int i = 0; i < G; ++i)
+            if (in[i]) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                x[i][j] -= mean;
-                if (in[i]) sq = __builtin_fmaf(x[i][j], x[i][j], sq);
+                for (int j = 0; j < V; ++j) {
+                    x[i][j] -= mean;
+                    sq = __builtin_fmaf(x[i][j], x[i][j], sq);
+                }
             }
-        const float rstd = 1.0f / sqrtf(team_sum<WPR>(sq, s_red[1]) / K + p.eps);
+        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(team_sum<WPR>(sq, s_red[1]), inv_k, p.eps));
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(NormArgs p) {
     __shared__ float s_red[2][WPR];
     __shared__ uint32_t s_max[WPR];
     const int64_t groups = p.K / V;
-    const float K = (float)p.K;
+    const float inv_k = 1.0f / (float)p.K;
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
         const uint16_t* row = p.x + m * p.K;
         float x[V], sum = 0.0f, sq = 0.0f;
@@ -140,13 +142,13 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(NormArgs p) {
 #pragma unroll
             for (int j = 0; j < V; ++j) sum += x[j];
         }
-        const float mean = team_sum<WPR>(sum, s_red[0]) / K;
+        const float mean = team_sum<WPR>(sum, s_red[0]) * inv_k;
         for (int64_t g = threadIdx.x; g < groups; g += 1024) {
             to_f32<V>(load_row_vec<V>(row, g), x);
 #pragma unroll
             for (int j = 0; j < V; ++j) sq = __builtin_fmaf(x[j] - mean, x[j] - mean, sq);
         }
-        const float rstd = 1.0f / sqrtf(team_sum<WPR>(sq, s_red[1]) / K + p.eps);
+        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(team_sum<WPR>(sq, s_red[1]), inv_k, p.eps));
         auto output = [&](int64_t g) {
             float w[V], b[V];
             load_f32<V>(p.w, g, 1.0f, w);
@@ -215,12 +217,12 @@ __device__ __forceinline__ XVec<V, CODES> load_x(const void* x, int64_t row, int
     }
     return r;
 }
-// x - mean: one exact conversion, then (for codes) c * (1 / a) in fp32, exact for a power of two
+// The bf16 values or the codes as fp32, exactly.
 template <int V, bool CODES>
-__device__ __forceinline__ void x_to_f32(const XVec<V, CODES>& v, float inv, float (&x)[V]) {
+__device__ __forceinline__ void x_to_f32(const XVec<V, CODES>& v, float (&x)[V]) {
     if constexpr (CODES) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = (float)(int8_t)(v.q[j / 4] >> (8 * (j & 3))) * inv;
+        for (int j = 0; j < V; ++j) x[j] = (float)(int8_t)(v.q[j / 4] >> (8 * (j & 3)));
     } else {
         to_f32<V>(v.v, x);
     }
@@ -278,17 +280,18 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void layernorm_back_kernel(
     for (int64_t m0 = (int64_t)blockIdx.x * TEAMS; m0 < p.M; m0 += step, parity ^= 1) {
         const int64_t m = m0 + team;
         load(m + step, nxt);
-        const float inv = CODES ? 1.0f / cur.inv : 1.0f;
+        // xh = (x - mean) rstd = x (rstd / a) - mean rstd in one fused multiply-add
+        const float scale = CODES ? cur.rstd / cur.inv : cur.rstd, shift = -cur.mean * cur.rstd;
         float xh[G][V], g[G][V], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             float d[V];
             to_f32<V>(cur.dy[i], d);
-            x_to_f32<V, CODES>(cur.x[i], inv, xh[i]);
+            x_to_f32<V, CODES>(cur.x[i], xh[i]);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 // columns past the row have dy = 0 and add nothing below
-                xh[i][j] = (xh[i][j] - cur.mean) * cur.rstd;
+                xh[i][j] = __builtin_fmaf(xh[i][j], scale, shift);
                 dw[i][j] = __builtin_fmaf(d[j], xh[i][j], dw[i][j]);
                 db[i][j] += d[j];
                 g[i][j] = d[j] * w[i][j];
@@ -312,7 +315,7 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void layernorm_back_kernel(
                 s2 += red[i][1];
             }
         }
-        const float c1 = s1 * inv_k, c2 = s2 * inv_k;
+        const float c1 = -cur.rstd * (s1 * inv_k), c2 = -cur.rstd * (s2 * inv_k);
         if (m < p.M) {
 #pragma unroll
             for (int i = 0; i < G; ++i) {
@@ -320,8 +323,8 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void layernorm_back_kernel(
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j)
                     o.w[j] = f32x2_to_bf16x2_rne(
-                        cur.rstd * __builtin_fmaf(-c2, xh[i][2 * j], g[i][2 * j] - c1),
-                        cur.rstd * __builtin_fmaf(-c2, xh[i][2 * j + 1], g[i][2 * j + 1] - c1));
+                        __builtin_fmaf(c2, xh[i][2 * j], __builtin_fmaf(cur.rstd, g[i][2 * j], c1)),
+                        __builtin_fmaf(c2, xh[i][2 * j + 1], __builtin_fmaf(cur.rstd, g[i][2 * j + 1], c1)));
                 if (in[i]) store_row_vec<V>(p.dx + m * p.K, lr + (int64_t)i * kStride, o);
             }
         }
@@ -369,16 +372,17 @@ __global__ __launch_bounds__(1024) void layernorm_back_long_kernel(NormBackArgs 
     const int64_t groups = p.K / V;
     const float inv_k = 1.0f / (float)p.K;
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
-        const float mean = p.mean[m], rstd = p.rstd[m], inv = CODES ? 1.0f / p.x_scale[m] : 1.0f;
+        const float mean = p.mean[m], rstd = p.rstd[m];
+        const float scale = CODES ? rstd / p.x_scale[m] : rstd, shift = -mean * rstd;
         float xh[V], g[V], s1 = 0.0f, s2 = 0.0f;
         auto read = [&](int64_t i) {
             float d[V], w[V];
             to_f32<V>(load_row_vec<V>(p.dy + m * p.K, i), d);
-            x_to_f32<V, CODES>(load_x<V, CODES>(p.x, m * p.K, i), inv, xh);
+            x_to_f32<V, CODES>(load_x<V, CODES>(p.x, m * p.K, i), xh);
             load_f32<V>(p.w, i, 1.0f, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                xh[j] = (xh[j] - mean) * rstd;
+                xh[j] = __builtin_fmaf(xh[j], scale, shift);
                 g[j] = d[j] * w[j];
             }
         };
@@ -416,7 +420,7 @@ __global__ __launch_bounds__(256) void layernorm_cols_kernel(NormBackArgs p) {
             x = (float)static_cast<const int8_t*>(p.x)[m * p.K + k] * (1.0f / p.x_scale[m]);
         else
             x = bf16_bits_to_f32(static_cast<const uint16_t*>(p.x)[m * p.K + k]);
-        dw += d * ((x - p.mean[m]) * p.rstd[m]);
+        dw = __builtin_fmaf(d, (x - p.mean[m]) * p.rstd[m], dw);
         db += d;
     }
     float* const part = p.part + (int64_t)blockIdx.y * 2 * p.K;
@@ -460,21 +464,36 @@ __global__ __launch_bounds__(1024) void layernorm_join_kernel(const float* __res
 }
 
 // ------------------------------------------------------------------------- dequantize
-// bf16(c / a): eight or four codes a thread, blocks of 256 groups along a row.
+// bf16(c * (1 / a)): V codes a thread, blocks of 256 groups along a row.
 template <int V>
 __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__ xq,
                                                       const float* __restrict__ a_scale, int64_t groups,
                                                       int64_t blocks_per_row, uint16_t* __restrict__ x) {
+    constexpr int P = V == 4 ? 4 : 8;  // codes per store
     const int64_t m = blockIdx.x / blocks_per_row;
     const int64_t g = (blockIdx.x - m * blocks_per_row) * 256 + threadIdx.x;
     if (g >= groups) return;
-    const float a = a_scale[m];
-    float f[V];
-    x_to_f32<V, true>(load_x<V, true>(xq, m * groups * V, g), 1.0f, f);
-    RowVec<V> o;
+    XVec<P, true> q[V / P];
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(xq + m * groups * V) + g * (V / 4);
+    if constexpr (V == 16) {
+        const uint4 t = *reinterpret_cast<const uint4*>(src);
+        q[0].q[0] = t.x;
+        q[0].q[1] = t.y;
+        q[1].q[0] = t.z;
+        q[1].q[1] = t.w;
+    } else {
+        q[0] = load_x<V, true>(xq, m * groups * V, g);
+    }
+    const float inv = 1.0f / a_scale[m];
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) o.w[j] = f32x2_to_bf16x2_rne(f[2 * j] / a, f[2 * j + 1] / a);
-    store_row_vec<V>(x + m * groups * V, g, o);
+    for (int i = 0; i < V / P; ++i) {
+        float f[P];
+        x_to_f32<P, true>(q[i], f);
+        RowVec<P> o;
+#pragma unroll
+        for (int j = 0; j < P / 2; ++j) o.w[j] = f32x2_to_bf16x2_rne(f[2 * j] * inv, f[2 * j + 1] * inv);
+        store_row_vec<P>(x + m * groups * V, g * (V / P) + i, o);
+    }
 }
 
 // Waves per row whose lanes hold the row in two groups each; 0: too long.
@@ -595,10 +614,13 @@ hipError_t launch_layernorm_back(const uint16_t* dy, const void* x, const float*
 
 hipError_t launch_dequant_act(const int8_t* xq, const float* a_scale, int64_t M, int64_t K, uint16_t* x,
                               hipStream_t stream) {
-    const int64_t groups = K / (K % 8 == 0 ? 8 : 4), bpr = (groups + 255) / 256;
+    const int V = K % 16 == 0 ? 16 : (K % 8 == 0 ? 8 : 4);
+    const int64_t groups = K / V, bpr = (groups + 255) / 256;
     if (M * bpr > INT32_MAX) return hipErrorInvalidValue;
     const dim3 grid((unsigned)(M * bpr)), block(256);
-    if (K % 8 == 0)
+    if (V == 16)
+        hipLaunchKernelGGL(dequant_kernel<16>, grid, block, 0, stream, xq, a_scale, groups, bpr, x);
+    else if (V == 8)
         hipLaunchKernelGGL(dequant_kernel<8>, grid, block, 0, stream, xq, a_scale, groups, bpr, x);
     else
         hipLaunchKernelGGL(dequant_kernel<4>, grid, block, 0, stream, xq, a_scale, groups, bpr, x);
