@@ -374,6 +374,9 @@ int bitnet_quant_gemv_b3(const uint16_t* x, const uint8_t* b3, const float* w_sc
  * dweight, dbias and dw instead of leaving them.  NULL is accepted where "optional" is said.
  * ================================================================================== */
 
+/* Most tokens of a product's gradients. */
+#define BITNET_GRAD_MAX_M (1 << 30)
+
 /* Scale of a token's int8 codes. */
 typedef enum {
     BITNET_SCALE_ABSMAX = 0, /* a = 127 / max(amax, 1e-5), as bitnet_quant_act            */
@@ -401,7 +404,7 @@ int bitnet_dequant_act(const int8_t* xq, const float* a_scale, int64_t M, int64_
  * bitnet_layernorm -- layer norm over K, with the int8 codes of its output fused in.
  *   mean[m] = mean_k x, rstd[m] = 1 / sqrt(mean_k (x - mean)^2 + eps),
  *   y = (x - mean) * rstd * weight + bias in fp32, rounded to bf16.
- *   weight, bias : float (K), optional (1 and 0).   eps > 0, finite.
+ *   weight, bias : float (K), optional (1 and 0).   eps: finite, normal, > 0.
  *   y            : bf16 (M, K), optional.
  *   xq, a_scale  : int8 (M, K) and float (M), both or neither: bit-identical to
  *                  bitnet_quant_act (scale = BITNET_SCALE_ABSMAX) or bitnet_quant_act_pow2
@@ -457,7 +460,8 @@ int bitnet_swiglu_backward(const uint16_t* dh, const void* g, const float* g_sca
  *   dx[m,k] = sum_g sum_n dy_g[m,n] * w_scale_g[n] * w_g[n,k].
  *   dy, packed, w_scale, N : HOST arrays of `groups` entries, read during the call only: bf16
  *                (M, N[g]), uint8 (N[g], K/4), float (N[g]) device pointers.  N[g] == 0 adds
- *                nothing; N[g] <= BITNET_MAX_K.  An unused code 0b11 counts as weight 0.
+ *                nothing; N[g] <= BITNET_MAX_K, M <= BITNET_GRAD_MAX_M.  An unused code 0b11
+ *                counts as weight 0.
  *   dx         : bf16 (M, K).  Each dy * w_scale is rounded to bf16 once, products with w and
  *                their sum are fp32, and the sum over all groups is rounded once.
  *   workspace  : optional scratch: with bitnet_grad_input_workspace_size bytes the sum is split
@@ -472,10 +476,10 @@ int bitnet_grad_input(int64_t M, int64_t K, int64_t groups, const uint16_t* cons
 /*
  * bitnet_grad_weight -- gradient with respect to the latent weights, from the forward's codes:
  *   dw[n,k] = sum_m dy[m,n] * xq[m,k] / a_scale[m].
- *   dy         : bf16 (M, N), N <= BITNET_MAX_K.
- *   xq, a_scale: int8 (M, K) and float (M).  Each xq / a is rounded to bf16 once; it is exact
- *                for power-of-two scales (bitnet_quant_act_pow2), and then only the fp32 sum
- *                and the output round.
+ *   dy         : bf16 (M, N), N <= BITNET_MAX_K, M <= BITNET_GRAD_MAX_M.
+ *   xq, a_scale: int8 (M, K) and float (M), positive.  Each xq * (1 / a) is rounded to bf16
+ *                once; it is exact for power-of-two scales (bitnet_quant_act_pow2), and then
+ *                only the fp32 sum and the output round.
  *   dw         : (N, K), BITNET_OUT_F32 or BITNET_OUT_BF16.
  *   workspace  : as in bitnet_grad_input.
  */

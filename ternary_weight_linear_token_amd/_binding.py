@@ -510,8 +510,9 @@ def _arg(t, dtype, name, shape, device):
 
 # Host time of a call counts at decode sizes: the raw getters below are what torch.cuda's
 # current_stream and current_device wrap (2.2 us a call with the wrappers, 0.3 without).
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
-_raw_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(name, device, *args):

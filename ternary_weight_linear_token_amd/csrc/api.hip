@@ -67,10 +67,11 @@ bool valid_dtype(int dt) {
 
 bool valid_scale(int s) { return s == BITNET_SCALE_ABSMAX || s == BITNET_SCALE_POW2; }
 
-// Shapes of a grouped input gradient: N[g] is the length summed over, at most BITNET_MAX_K
-// (the kernels' 32-bit offsets into a block of rows).
+// Shapes of a gradient: N[g] at most BITNET_MAX_K (the kernels' 32-bit offsets into a block
+// of rows), M at most 2^30 (their 32-bit row numbers, padded to a tile).
 int check_grad_groups(int64_t M, int64_t K, int64_t groups, const int64_t* N) {
     if (groups < 1 || groups > BITNET_MAX_GROUPS || !N) return BITNET_ERR_INVALID_ARG;
+    if (M > BITNET_GRAD_MAX_M) return BITNET_ERR_INVALID_ARG;
     for (int64_t g = 0; g < groups; ++g) {
         const int st = check_shape(M, N[g], K);
         if (st) return st;
@@ -501,7 +502,7 @@ int bitnet_layernorm(const uint16_t* x, const float* weight, const float* bias, 
                      int64_t M, int64_t K, uint16_t* y, int8_t* xq, float* a_scale, int scale,
                      float* mean, float* rstd, void* stream) {
     if (!valid_scale(scale)) return BITNET_ERR_INVALID_ARG;
-    if (!(eps > 0.0f) || eps > FLT_MAX) return BITNET_ERR_INVALID_ARG;
+    if (!(eps >= FLT_MIN) || eps > FLT_MAX) return BITNET_ERR_INVALID_ARG;
     int st = check_shape(M, 0, K);
     if (st) return st;
     if (M == 0) return BITNET_OK;
@@ -615,7 +616,7 @@ int bitnet_grad_plan(int weight, int64_t M, int64_t K, int64_t groups, const int
 }
 
 size_t bitnet_grad_weight_workspace_size(int64_t M, int64_t N, int64_t K) {
-    if (check_shape(M, N, K) != BITNET_OK || M == 0 || N == 0 || N > BITNET_MAX_K) return 0;
+    if (check_grad_groups(M, K, 1, &N) != BITNET_OK || M == 0 || N == 0) return 0;
     return bitnet::grad_weight_workspace_size(M, N, K);
 }
 
@@ -623,9 +624,8 @@ int bitnet_grad_weight(const uint16_t* dy, const int8_t* xq, const float* a_scal
                        int64_t N, int64_t K, void* dw, int out_dtype, void* workspace,
                        size_t ws_bytes, void* stream) {
     if (out_dtype != BITNET_OUT_F32 && out_dtype != BITNET_OUT_BF16) return BITNET_ERR_INVALID_ARG;
-    int st = check_shape(M, N, K);
+    int st = check_grad_groups(M, K, 1, &N);
     if (st) return st;
-    if (N > BITNET_MAX_K) return BITNET_ERR_INVALID_ARG;
     if (N == 0) return BITNET_OK;
     if (!dw || (ws_bytes > 0 && !workspace)) return BITNET_ERR_INVALID_ARG;
     if (M > 0 && (!dy || !xq || !a_scale)) return BITNET_ERR_INVALID_ARG;

@@ -50,7 +50,7 @@ def test_layernorm_validation(L):
     assert f(y=None, xq=None, a=None) == INVALID      # nothing to write
     assert f(a=None) == INVALID and f(xq=None) == INVALID  # codes and scales go together
     assert f(scale=2) == INVALID and f(scale=-1) == INVALID
-    for eps in (0.0, -1e-5, float("inf"), float("nan")):
+    for eps in (0.0, -1e-5, 1e-39, float("inf"), float("nan")):
         assert f(eps=eps) == INVALID
     assert f(K=255) == UNALIGNED and f(K=0) == INVALID and f(K=(1 << 20) + 4) == INVALID
     assert f(M=-1) == INVALID and f(M=1 << 31) == INVALID
@@ -114,6 +114,7 @@ def test_grad_input_validation(L):
     assert f(K=250) == UNALIGNED and f(K=0) == INVALID
     assert f(N=i64s(16, -1)) == INVALID and f(N=i64s(16, (1 << 20) + 1)) == INVALID
     assert f(M=-1) == INVALID and f(M=0, dx=None) == OK
+    assert f(M=(1 << 30) + 1) == INVALID
     assert L.bitnet_grad_input_workspace_size(4, 250, 2, i64s(16, 32)) == 0
     assert L.bitnet_grad_input_workspace_size(4, 256, 0, i64s(16, 32)) == 0
 
@@ -127,7 +128,7 @@ def test_grad_weight_validation(L):
     assert f(dt=2) == INVALID and f(dt=-1) == INVALID
     assert f(ws=None, n=16) == INVALID and f(ws=A + 4, n=16) == UNALIGNED
     assert f(K=254) == UNALIGNED and f(N=(1 << 20) + 1) == INVALID and f(N=-1) == INVALID
-    assert f(N=0, dw=None) == OK
+    assert f(N=0, dw=None) == OK and f(M=(1 << 30) + 1) == INVALID
     assert L.bitnet_grad_weight_workspace_size(4, 16, 254) == 0
     assert L.bitnet_grad_weight_workspace_size(0, 16, 256) == 0
 
