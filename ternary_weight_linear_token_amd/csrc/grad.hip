@@ -310,7 +310,11 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
         if constexpr (MODE == 0) {
             const int n = i / 9, h = i % 9 - 1;
             if (h < 0) {
-                inv = v.s[n] > 0.0f ? 1.0f / v.s[n] : 0.0f;  // rows past the end: scale 0
+                // 1 / a: the reciprocal (1 ulp) and one Newton step, which leaves 2^-46 before its
+                // rounding and keeps powers of two exact, in a third of a division's
+                // instructions.  Rows past the end: scale 0.
+                const float a = v.s[n], r = __builtin_amdgcn_rcpf(a);
+                inv = a > 0.0f ? __builtin_fmaf(__builtin_fmaf(-a, r, 1.0f), r, r) : 0.0f;
             } else {
                 // (c + 128) inv - 128 inv: a byte and 128 inv are exact in fp32, so each value
                 // is rounded once (not at all for a power of two)
