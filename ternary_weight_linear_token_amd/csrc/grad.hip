@@ -316,12 +316,11 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
                 const float a = v.s[n], r = __builtin_amdgcn_rcpf(a);
                 inv = a > 0.0f ? __builtin_fmaf(__builtin_fmaf(-a, r, 1.0f), r, r) : 0.0f;
             } else {
-                // (c + 128) inv - 128 inv: a byte and 128 inv are exact in fp32, so each value
-                // is rounded once (not at all for a power of two)
-                const uint32_t u = (v.b[n][h >> 1] ^ 0x80808080u) >> (16 * (h & 1));
-                const float off = -128.0f * inv;
-                half_out[h >> 2][h & 3] = f32x2_to_bf16x2_rne(__builtin_fmaf((float)(u & 0xFFu), inv, off),
-                                                              __builtin_fmaf((float)((u >> 8) & 0xFFu), inv, off));
+                // each value rounded once (not at all for a power of two)
+                const uint32_t u = v.b[n][h >> 1];
+                const float f0 = (float)(int8_t)(u >> (16 * (h & 1)));
+                const float f1 = (float)(int8_t)(u >> (16 * (h & 1) + 8));
+                half_out[h >> 2][h & 3] = f32x2_to_bf16x2_rne(f0 * inv, f1 * inv);
             }
             if (h == 7) {
                 const int id = tg + n * TG;
