@@ -39,8 +39,16 @@
 //    mask; rows that start off a dword are put together from the dwords around them; columns
 //    past i or j are computed from whatever lies there and never stored (they only reach
 //    their own outputs).
-// Measured (dx and dw, bf16 out): 8192^3 1334 and 1150 TFLOP/s (a library bf16 product of that
-// size: 1264), the matrix cores busy half of the time.
+// Measured in one run (bf16 out; beside it a library's bf16 product, 1211 TFLOP/s at 8192^3 and
+// 872 to 901 on transposed left operands like dw's): dx 8192^3 857 us, 1283 TFLOP/s, the matrix
+// cores busy 56% of the cycles at 4096^3 (the chip holds about 1.8 GHz under such a load, where
+// the peak is 1.9 PFLOP/s); dw 8192^3 981 us, 1121 TFLOP/s, 49%: both operands of dw are read
+// transposed as bf16, 192 KB of LDS reads a step against 132 KB.  What is left is the vector
+// instructions of the conversion, which the matrix instructions hide in part.
+// One token to dozens: dx 4 x 2560 x 2560 5.7 us and 2.0 to 3.4 for the join, launch and
+// latency; 512 x 3840 x 2560 25 us against 7.3 at the rate of a large product: 160 tiles on 256
+// CUs and a chain of 30 short steps.  dw 512 x 6912 x 2560 fp32 40 us against 16.3 for its
+// 79 MB: 1080 tiles on 1024 places leave a last round of 56.
 #include <cmath>
 #include <utility>
 
