@@ -135,7 +135,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     constexpr int kJoin = G > 1 ? (G / 2) * WPG * WM * WN * 4 : 0;
     constexpr int kLds = 2 * G * kBuf > kJoin ? 2 * G * kBuf : kJoin;
     static_assert(kLds <= 160 * 1024, "LDS");
-    static_assert(WN == 64 || WN == 128, "columns of a wave");
+    static_assert(WN == 64, "a wave's 64 columns are 16 byte columns of packed weights");
     static_assert(KS % 2 == 0, "operand sets alternate");
     // 16-byte loads of A, 16 codes or 16 weights of B per thread and step
     constexpr int kAUnits = BM * BL / 8, kBUnits = BN * BL / 16;
@@ -365,9 +365,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
             off_a[ks] = chunk<BL>(wi * WM + (lane & 31), 2 * ks + (lane >> 5));
-        // 8-bit transposed reads: row l8 + t16 / 2, 8 bytes t16 % 2 of a 16-byte column.  WN 64:
-        // both halves of the lanes read the wave's 16 byte columns; WN 128: one 16 each.
-        off_b[0] = packed_at<BN>(l8 + (t16 >> 1), WN == 64 ? wj : 2 * wj + half) + 8 * (t16 & 1);
+        // 8-bit transposed reads: row l8 + t16 / 2, 8 bytes t16 % 2 of the wave's 16 byte columns,
+        // the same for both halves of the lanes (they take other fields of them)
+        off_b[0] = packed_at<BN>(l8 + (t16 >> 1), wj) + 8 * (t16 & 1);
     }
     auto tr16 = [&](const uint8_t* a, int rows4) {
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a));
@@ -394,12 +394,13 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
                 o.a[r - 1] = *reinterpret_cast<const bf16x8*>(A + off_a[ks] + (r - 1) * 32 * 2 * BL);
         }
     };
-    // MODE 1: four of the eight weights of b[j] (field 2 j + half of the byte column for WN 64,
-    // j for WN 128), the 2 NJ parts of a step's 16 rows.
+    // MODE 1: four of the eight weights of b[j] (field 2 j + half of the byte column), the 2 NJ
+    // parts of a step's 16 rows: a lookup gives the high bytes of bf16(2w), whose low bytes
+    // are zero.
     auto expand = [&](Operands& o, int part) {
         const int j = part >> 1, i = part & 1;
         const uint32_t hi = __builtin_amdgcn_perm(
-            kHi2w, kHi2w, ((uint32_t)o.w[i] >> (WN == 64 ? 4 * j + 2 * half : 2 * j)) & 0x03030303u);
+            kHi2w, kHi2w, ((uint32_t)o.w[i] >> (4 * j + 2 * half)) & 0x03030303u);
         u32x4 x = __builtin_bit_cast(u32x4, o.b[j]);
         x[2 * i] = __builtin_amdgcn_perm(0u, hi, 0x010C000Cu);
         x[2 * i + 1] = __builtin_amdgcn_perm(0u, hi, 0x030C020Cu);
@@ -529,8 +530,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     }
 
     // lane l, register r of a 32x32 accumulator: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
-    // MODE 0: block j holds columns 32 j + l % 32.  MODE 1: byte column l % 16 (WN 64) or l % 32
-    // (WN 128) of the wave, its weight 2 j + half or j.
+    // MODE 0: block j holds columns 32 j + l % 32.  MODE 1: byte column l % 16 of the wave, its
+    // weight 2 j + half.
     float* const part = p.part + (int64_t)slice * I * J;
     const int jw = j0 + wj * WN;
 #pragma unroll
@@ -552,7 +553,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
                             static_cast<uint16_t*>(p.out)[o + col] = f32_to_bf16_rne(acc[i][j][r]);
                     }
                 }
-            } else if constexpr (WN == 64) {
+            } else {
                 // lanes l and l + 16 hold columns 4 t + (0, 2) and 4 t + (1, 3): exchange, so that a
                 // lane has two neighbours, 4 t + 2 half + (0, 1)
                 const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][0][r]),
@@ -565,17 +566,6 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
                     else
                         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o + col) =
                             f32x2_to_bf16x2_rne(v0, v1);
-                }
-            } else {
-                const int col = jw + 4 * (lane & 31);
-                const float4 v = make_float4(0.5f * acc[i][0][r], 0.5f * acc[i][1][r],
-                                             0.5f * acc[i][2][r], 0.5f * acc[i][3][r]);
-                if (row < I && col < J) {
-                    if (p.slices > 1)
-                        *reinterpret_cast<float4*>(part + o + col) = v;
-                    else
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o + col) =
-                            make_uint2(f32x2_to_bf16x2_rne(v.x, v.y), f32x2_to_bf16x2_rne(v.z, v.w));
                 }
             }
         }

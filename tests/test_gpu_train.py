@@ -516,6 +516,42 @@ def test_product_gradients_against_differences():
     assert (num - (dw.double() * v).sum()).abs() <= (M + 64) * U * (size * v.abs()).sum()
 
 
+def test_offsets_past_32_bits():
+    # more than 2^31 elements: the last rows come out as they do alone
+    M, N, K, T = 1_100_003, 2048, 64, 5
+    dy = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    tail = bf16(T, N, seed=1, hot=False)
+    dy[-T:] = tail
+    xq = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+    a = torch.ones((M,), device="cuda")
+    tq, ta = bw.quant_act_pow2(bf16(T, K, seed=2))
+    xq[-T:], a[-T:] = tq, ta
+    # zero rows add exact zeros: the sum of five products in some order
+    check_grad_weight(tail, tq, ta, "f32", bw.grad_weight(dy, xq, a), "dw")
+    p, s = ternary(N, K)
+    dx = bw.grad_input(dy, p, s)
+    check_grad_input([tail], [p], [s], K, dx[-T:], "dx")
+    assert not dx[:-T].any()
+    del dx
+    # dy as a norm's input, and as SwiGLU's
+    y, mean, rstd = bw.layernorm(dy, return_stats=True)
+    check_norm(tail, None, None, y[-T:], mean[-T:], rstd[-T:], "norm")
+    assert not y[:-T].any()
+    gx, gw, gb = bw.layernorm_backward(y, dy, None, mean, rstd)
+    rx, rw, rb, size, sw, sb = norm_back64(y[-T:], tail, None, mean[-T:], rstd[-T:])
+    close(gx[-T:], rx, BF * rx.abs() + 72 * U * size + TINY, "norm dx")
+    # 1.1 million rows over 512 blocks: 2149 more additions, of zeros, on the path
+    close(gw, rw, 136 * U * sw + TINY, "norm dweight")
+    del gx, y
+    h, (gq, uq, gs, us) = bw.swiglu(dy, dy, checkpoint=True)
+    check_swiglu(tail, tail, h[-T:], "swiglu")
+    dg, du = bw.swiglu_backward(dy, gq, uq, gs, us)
+    v = gq[-T:].double() / gs[-T:].double()[:, None]
+    check_swiglu_back(tail, v, v, dg[-T:], du[-T:], "swiglu backward")
+    q, sc = bw.quant_act_pow2(dy)
+    assert torch.equal(bw.dequant_act(q, sc)[-T:].double(), q[-T:].double() / sc[-T:].double()[:, None])
+
+
 # ------------------------------------------------------------------- the set as it is used
 
 def mlp_step(x, dy, w, b, gate, up, down, outs=None):
