@@ -50,6 +50,7 @@
 // CUs and a chain of 30 short steps.  dw 512 x 6912 x 2560 fp32 40 us against 16.3 for its
 // 79 MB: 1080 tiles on 1024 places leave a last round of 56.
 #include <cmath>
+#include <type_traits>
 #include <utility>
 
 #include "device_common.hpp"
@@ -532,43 +533,66 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     // lane l, register r of a 32x32 accumulator: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
     // MODE 0: block j holds columns 32 j + l % 32.  MODE 1: byte column l % 16 of the wave, its
     // weight 2 j + half.
-    float* const part = p.part + (int64_t)slice * I * J;
-    const int jw = j0 + wj * WN;
+    // The kind of output and whether the tile lies inside it are the same for the whole block,
+    // so they are asked once; 32-bit offsets reach over a tile's rows (256 rows of 2^20).
+    // (The empty asm keeps the offsets from being computed, and held in registers, before the
+    // main loop.)
+    int pitch = J, tid_out = lane;
+    asm volatile("" : "+s"(pitch), "+v"(tid_out));
+    const int64_t base = (int64_t)(i0 + wi * WM) * pitch + j0 + wj * WN;
+    const int rows = I - i0 - wi * WM, cols = J - j0 - wj * WN;
+    const bool inside = rows >= WM && cols >= WN;
+    auto emit = [&](auto all, auto put) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = i0 + wi * WM + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-            const int64_t o = (int64_t)row * J;
-            if constexpr (MODE == 0) {
+            for (int r = 0; r < 16; ++r) {
+                const int row = 32 * i + 8 * (r >> 2) + 4 * (tid_out >> 5) + (r & 3);
+                if constexpr (MODE == 0) {
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const int col = jw + 32 * j + (lane & 31);
-                    if (row < I && col < J) {
-                        if (p.slices > 1)
-                            part[o + col] = acc[i][j][r];
-                        else if (p.out_dtype == BITNET_OUT_F32)
-                            static_cast<float*>(p.out)[o + col] = acc[i][j][r];
-                        else
-                            static_cast<uint16_t*>(p.out)[o + col] = f32_to_bf16_rne(acc[i][j][r]);
+                    for (int j = 0; j < NJ; ++j) {
+                        const int col = 32 * j + (tid_out & 31);
+                        if (decltype(all)::value || (row < rows && col < cols))
+                            put((uint32_t)(row * pitch + col), acc[i][j][r], 0.0f);
                     }
-                }
-            } else {
-                // lanes l and l + 16 hold columns 4 t + (0, 2) and 4 t + (1, 3): exchange, so that a
-                // lane has two neighbours, 4 t + 2 half + (0, 1)
-                const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][0][r]),
-                                                                __float_as_uint(acc[i][1][r]), false, false);
-                const float v0 = 0.5f * __uint_as_float(x[0]), v1 = 0.5f * __uint_as_float(x[1]);
-                const int col = jw + 4 * t16 + 2 * half;
-                if (row < I && col < J) {
-                    if (p.slices > 1)
-                        *reinterpret_cast<float2*>(part + o + col) = make_float2(v0, v1);
-                    else
-                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o + col) =
-                            f32x2_to_bf16x2_rne(v0, v1);
+                } else {
+                    // lanes l and l + 16 hold columns 4 t + (0, 2) and 4 t + (1, 3): exchange, so
+                    // that a lane has two neighbours, 4 t + 2 half + (0, 1)
+                    const auto x = __builtin_amdgcn_permlane16_swap(
+                        __float_as_uint(acc[i][0][r]), __float_as_uint(acc[i][1][r]), false, false);
+                    const int col = 4 * (tid_out & 15) + 2 * ((tid_out >> 4) & 1);
+                    if (decltype(all)::value || (row < rows && col < cols))
+                        put((uint32_t)(row * pitch + col), 0.5f * __uint_as_float(x[0]),
+                            0.5f * __uint_as_float(x[1]));
                 }
             }
-        }
+    };
+    auto output = [&](auto put) {
+        if (inside)
+            emit(std::true_type(), put);
+        else
+            emit(std::false_type(), put);
+    };
+    if (p.slices > 1) {
+        float* const out = p.part + (int64_t)slice * I * J + base;
+        output([&](uint32_t o, float v0, float v1) {
+            if constexpr (MODE == 0)
+                out[o] = v0;
+            else
+                *reinterpret_cast<float2*>(out + o) = make_float2(v0, v1);
+        });
+    } else if (MODE == 0 && p.out_dtype == BITNET_OUT_F32) {
+        float* const out = static_cast<float*>(p.out) + base;
+        output([&](uint32_t o, float v0, float) { out[o] = v0; });
+    } else {
+        uint16_t* const out = static_cast<uint16_t*>(p.out) + base;
+        output([&](uint32_t o, float v0, float v1) {
+            if constexpr (MODE == 0)
+                out[o] = f32_to_bf16_rne(v0);
+            else
+                *reinterpret_cast<uint32_t*>(out + o) = f32x2_to_bf16x2_rne(v0, v1);
+        });
+    }
 }
 
 // Sum of the slices' partials, in order; four outputs a thread (J % 4 == 0).
