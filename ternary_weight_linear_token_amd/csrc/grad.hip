@@ -39,15 +39,15 @@
 //    mask; rows that start off a dword are put together from the dwords around them; columns
 //    past i or j are computed from whatever lies there and never stored (they only reach
 //    their own outputs).
-// Measured in one run (bf16 out; beside it a library's bf16 product, 1211 TFLOP/s at 8192^3 and
-// 872 to 901 on transposed left operands like dw's): dx 8192^3 857 us, 1283 TFLOP/s, the matrix
+// Measured in one run (bf16 out; beside it a library's bf16 product, 1250 TFLOP/s at 8192^3 and
+// 887 to 935 on transposed left operands like dw's): dx 8192^3 830 us, 1326 TFLOP/s, the matrix
 // cores busy 56% of the cycles at 4096^3 (the chip holds about 1.8 GHz under such a load, where
-// the peak is 1.9 PFLOP/s); dw 8192^3 981 us, 1121 TFLOP/s, 49%: both operands of dw are read
+// the peak is 1.9 PFLOP/s); dw 8192^3 906 us, 1214 TFLOP/s: both operands of dw are read
 // transposed as bf16, 192 KB of LDS reads a step against 132 KB.  What is left is the vector
 // instructions of the conversion, which the matrix instructions hide in part.
 // One token to dozens: dx 4 x 2560 x 2560 5.7 us and 2.0 to 3.4 for the join, launch and
-// latency; 512 x 3840 x 2560 25 us against 7.3 at the rate of a large product: 160 tiles on 256
-// CUs and a chain of 30 short steps.  dw 512 x 6912 x 2560 fp32 40 us against 16.3 for its
+// latency; 512 x 3840 x 2560 24 us against 7.3 at the rate of a large product: 160 tiles on 256
+// CUs and a chain of 30 short steps.  dw 512 x 6912 x 2560 fp32 35 us against 16.3 for its
 // 79 MB: 1080 tiles on 1024 places leave a last round of 56.
 #include <cmath>
 #include <type_traits>
@@ -629,10 +629,11 @@ struct GradCfg {
     double base, step_alone, step_full;
 };
 constexpr GradCfg kCfg[] = {
-    // weight gradient.  256 x 256 is the fastest per flop (2048 x 4096 x 14336: 262 us, 128 x 128
-    // tiles 305); its 256 blocks at a time leave most of the chip idle in a short last round
-    // (512 x 6912 x 2560, 270 tiles: 53 us), which 128 x 128 tiles, two or four blocks per CU,
-    // fill better (45 and 43 us); four share a CU only at half the rows per step.
+    // weight gradient (times and costs taken before the epilogue lost its branches, which takes
+    // 10 to 15% off all three).  256 x 256 is the fastest per flop (2048 x 4096 x 14336: 262 us,
+    // 128 x 128 tiles 305); its 256 blocks at a time leave most of the chip idle in a short last
+    // round (512 x 6912 x 2560, 270 tiles: 53 us), which 128 x 128 tiles, two or four blocks per
+    // CU, fill better (45 and 43 us); four share a CU only at half the rows per step.
     {0, 256, 256, 128, 64, 1, 64, 1, 1, 1, 13, 1.8, 1.8},
     {0, 128, 128, 64, 64, 1, 64, 1, 1, 2, 8, 0.73, 1.15},
     {0, 128, 128, 64, 64, 1, 32, 1, 4, 4, 8, 0.43, 1.25},
