@@ -35,10 +35,12 @@
 //    scalar instructions a step cost 8% at 8192^3.
 //  * Few output tiles: l is also split over blocks (slices); every slice writes fp32 partial
 //    sums to the workspace and a second launch adds them in a fixed order.
-//  * Tails: rows past the end of l read as zeros through the buffer descriptors' bounds or a
-//    mask; rows that start off a dword are put together from the dwords around them; columns
-//    past i or j are computed from whatever lies there and never stored (they only reach
-//    their own outputs).
+//  * Tails: what lies past the end of l reads as zeros through the buffer descriptors' bounds
+//    or a mask.  Rows that start off a dword are put together from the dwords around them, and
+//    the last of these may hold one value more than the tensor: rows past the end are then
+//    sent out of bounds by their number (a zero in the other operand is not enough, 0 x NaN is
+//    NaN).  Columns past i or j are computed from whatever lies there and never stored (they
+//    only reach their own outputs).
 // Measured in one run (bf16 out; beside it a library's bf16 product, 1250 TFLOP/s at 8192^3 and
 // 887 to 935 on transposed left operands like dw's): dx 8192^3 830 us, 1326 TFLOP/s, the matrix
 // cores busy 56% of the cycles at 4096^3 (the chip holds about 1.8 GHz under such a load, where
@@ -264,7 +266,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     Loads ld[D];
     auto load_a = [&](Loads& v, int n) {
         if constexpr (MODE == 0) {
-            v.a[n] = ALIGNED ? load16(ra, voff_a[n]) : load8_half(ra, voff_a[n], 0);
+            if (ALIGNED)
+                v.a[n] = load16(ra, voff_a[n]);
+            else  // the rounded descriptor reaches into the row behind the last one
+                v.a[n] = load8_half(ra, (tg + n * TG) / (BM / 8) < left ? voff_a[n] : 0x80000000u, 0);
         } else {
             if (ALIGNED) {  // whole chunks: those past the row's end read as zeros
                 const bool in = 8 * (tg % (BL / 8)) < left;
