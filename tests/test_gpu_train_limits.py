@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import ternary_weight_linear_token_amd as bw
-from test_gpu_train import bf16
+from test_gpu_train import BF, TINY, U, bf16, close, f32
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +26,46 @@ def test_grad_weight_of_a_prefix(M, N, K, dt):
         assert torch.equal(bw.grad_weight(big[:M], xq, a, out_dtype=dt), clean), value
         assert torch.equal(bw.grad_weight(big[:M], xq, a, out_dtype=dt, workspace=False),
                            bw.grad_weight(big[:M].clone(), xq, a, out_dtype=dt, workspace=False)), value
+
+
+# --------------------------------------------------------------------- rows far from zero
+
+def norm_back_xh(dy, x64, w, mean, rstd):
+    """dx, dweight in 64 bits and the sizes that roundings relative to xh are counted against."""
+    dy, w, mean, rstd = dy.double(), w.double(), mean.double(), rstd.double()
+    xh = (x64 - mean[:, None]) * rstd[:, None]
+    g = dy * w
+    dx = rstd[:, None] * (g - g.mean(1, keepdim=True) - xh * (g * xh).mean(1, keepdim=True))
+    size = rstd[:, None] * (g.abs() + g.abs().mean(1, keepdim=True) +
+                            xh.abs() * (g * xh).abs().mean(1, keepdim=True))
+    return dx, (dy * xh).sum(0), size, (dy * xh).abs().sum(0)
+
+
+# xh = (x - mean) * rstd has one rounding in the difference and one in the product, relative to
+# xh itself; from codes (c - a mean) (rstd / a) has three.  Its terms of dweight then add up
+# along a path under 128: 131 u.  dx: 64 for a path, g, 3 for xh, 1 / K, two products, xh again
+# and the last two sums: under 80 u.  Nothing is relative to the mean.
+@pytest.mark.parametrize("K", [252, 1028, 2560, 8192, 14336, 20000])
+@pytest.mark.parametrize("kind", ["bf16", "pow2", "absmax"])
+def test_norm_backward_far_from_zero(K, kind):
+    M = 6
+    x = bf16(M, K, seed=K, hot=False)
+    for m, shift in enumerate((0.0, 5.0, -50.0, 500.0, 8000.0)):
+        x[m] += shift
+    x[5] = 3.0
+    dy = bf16(M, K, seed=K + 1, scale=1e-3)
+    w = f32(K, seed=1, scale=0.2, shift=1.0)
+    mean = x.double().mean(1).float()
+    rstd = ((x.double() - mean.double()[:, None]).square().mean(1) + 1e-5).rsqrt().float()
+    scale = None
+    x64, arg = x.double(), x
+    if kind != "bf16":
+        arg, scale = (bw.quant_act_pow2 if kind == "pow2" else bw.quant_act)(x)
+        x64 = arg.double() / scale.double()[:, None]
+    for rows in ([0], [1], [2], [3], [4], [5], list(range(M))):
+        r = torch.tensor(rows, device="cuda")
+        s = None if scale is None else scale[r]
+        dx, dw, _ = bw.layernorm_backward(dy[r], arg[r], w, mean[r], rstd[r], x_scale=s)
+        rx, rw, size, sw = norm_back_xh(dy[r], x64[r], w, mean[r], rstd[r])
+        close(dx, rx, BF * rx.abs() + (1 + BF) * 80 * U * size + TINY, f"{K} {kind} {rows} dx")
+        close(dw, rw, 131 * U * sw + TINY, f"{K} {kind} {rows} dweight")
