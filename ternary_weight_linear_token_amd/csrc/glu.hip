@@ -115,26 +115,29 @@ __global__ __launch_bounds__(64 * WPR) void swiglu_kernel(GluArgs p) {
             }
             if (p.hq) p.h_scale[m] = ah;
         }
-        auto store = [&](int64_t q, const RowVec<V>& gv, const RowVec<V>& uv, const RowVec<V>& hv) {
-            if (p.gq) {
-                store_codes<V>(p.gq + row, q, gv, ag);
-                store_codes<V>(p.uq + row, q, uv, au);
-            }
-            if (p.hq) store_codes<V>(p.hq + row, q, hv, ah);
-        };
-        if (G > 0) {
+        with_clamp(max(max(mg, mu), mh), [&](auto clamp) {
+            constexpr bool C = decltype(clamp)::value;
+            auto store = [&](int64_t q, const RowVec<V>& gv, const RowVec<V>& uv, const RowVec<V>& hv) {
+                if (p.gq) {
+                    store_codes<V, C>(p.gq + row, q, gv, ag);
+                    store_codes<V, C>(p.uq + row, q, uv, au);
+                }
+                if (p.hq) store_codes<V, C>(p.hq + row, q, hv, ah);
+            };
+            if (G > 0) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const int64_t q = threadIdx.x + (int64_t)i * kStride;
-                if (q < groups) store(q, g[i], u[i], h[i]);
+                for (int i = 0; i < H; ++i) {
+                    const int64_t q = threadIdx.x + (int64_t)i * kStride;
+                    if (q < groups) store(q, g[i], u[i], h[i]);
+                }
+            } else {
+                for (int64_t q = threadIdx.x; q < groups; q += kStride) {
+                    g[0] = load_row_vec<V>(p.g + row, q);
+                    u[0] = load_row_vec<V>(p.u + row, q);
+                    store(q, g[0], u[0], swiglu_vec<V>(g[0], u[0]));
+                }
             }
-        } else {
-            for (int64_t q = threadIdx.x; q < groups; q += kStride) {
-                g[0] = load_row_vec<V>(p.g + row, q);
-                u[0] = load_row_vec<V>(p.u + row, q);
-                store(q, g[0], u[0], swiglu_vec<V>(g[0], u[0]));
-            }
-        }
+        });
     }
 }
 

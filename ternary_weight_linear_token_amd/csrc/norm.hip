@@ -121,11 +121,16 @@ __global__ __launch_bounds__(64 * WPR) void layernorm_kernel(NormArgs p) {
             if (p.rstd) p.rstd[m] = rstd;
         }
         if (p.xq) {
-            const float a = scale_of(team_max<WPR>(max_of_pair(mx), s_max), p.pow2);
+            const uint32_t amax = team_max<WPR>(max_of_pair(mx), s_max);
+            const float a = scale_of(amax, p.pow2);
             if (threadIdx.x == 0) p.a_scale[m] = a;
+            with_clamp(amax, [&](auto clamp) {
 #pragma unroll
-            for (int i = 0; i < G; ++i)
-                if (in[i]) store_codes<V>(p.xq + m * p.K, threadIdx.x + (int64_t)i * kStride, cur[i], a);
+                for (int i = 0; i < G; ++i)
+                    if (in[i])
+                        store_codes<V, decltype(clamp)::value>(p.xq + m * p.K, threadIdx.x + (int64_t)i * kStride,
+                                                               cur[i], a);
+            });
         }
 #pragma unroll
         for (int i = 0; i < G; ++i) cur[i] = nxt[i];
@@ -180,10 +185,13 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(NormArgs p) {
             if (p.rstd) p.rstd[m] = rstd;
         }
         if (p.xq) {
-            const float a = scale_of(team_max<WPR>(max_of_pair(mx), s_max), p.pow2);
+            const uint32_t amax = team_max<WPR>(max_of_pair(mx), s_max);
+            const float a = scale_of(amax, p.pow2);
             if (threadIdx.x == 0) p.a_scale[m] = a;
-            for (int64_t g = threadIdx.x; g < groups; g += 1024)
-                store_codes<V>(p.xq + m * p.K, g, output(g), a);
+            with_clamp(amax, [&](auto clamp) {
+                for (int64_t g = threadIdx.x; g < groups; g += 1024)
+                    store_codes<V, decltype(clamp)::value>(p.xq + m * p.K, g, output(g), a);
+            });
         }
     }
 }

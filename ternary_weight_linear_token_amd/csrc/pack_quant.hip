@@ -120,34 +120,6 @@ __global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__
 // pass 1 only and leaves the row's max magnitude bits in a_scale[m]; tensor_scale_kernel
 // reduces them and writes the common scale to every a_scale[m]; MODE 2 runs pass 2 with
 // the scale read from a_scale[m].  MODE 3: as MODE 0 with a power-of-two scale.
-template <int V>
-struct QVec {
-    uint32_t w[V / 2];  // V bf16 values, two per word, low half first
-};
-
-template <int V>
-__device__ __forceinline__ QVec<V> load_qvec(const uint16_t* row, int64_t g) {
-    QVec<V> v;
-    if constexpr (V == 8) {
-        const uint4 t = reinterpret_cast<const uint4*>(row)[g];
-        v.w[0] = t.x; v.w[1] = t.y; v.w[2] = t.z; v.w[3] = t.w;
-    } else {
-        const uint2 t = reinterpret_cast<const uint2*>(row)[g];
-        v.w[0] = t.x; v.w[1] = t.y;
-    }
-    return v;
-}
-
-template <int V>
-__device__ __forceinline__ uint32_t qvec_max_bits(const QVec<V>& v, uint32_t mx) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        const uint32_t a = v.w[i] & 0x7FFF7FFFu;
-        mx = max(mx, max(a & 0xFFFFu, a >> 16));
-    }
-    return mx;
-}
-
 template <int G, int MODE, int V, int WPR>
 __global__ __launch_bounds__(256) void quant_act_kernel(const uint16_t* __restrict__ x,
                                                         int64_t M, int64_t K,
@@ -167,31 +139,27 @@ __global__ __launch_bounds__(256) void quant_act_kernel(const uint16_t* __restri
     const int64_t groups = live ? K / V : 0;
     const uint16_t* row = x + (live ? m : 0) * K;
 
-    QVec<V> held[G > 0 ? G : 1];
-    uint32_t mx = 0;
+    RowVec<V> held[G > 0 ? G : 1];
+    uint32_t mx = 0;  // of the two halves of the words, then of the row
     if (G > 0) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             const int64_t g = lr + (int64_t)i * kStride;
-            if (g < groups) {
-                held[i] = load_qvec<V>(row, g);
-            } else {
-#pragma unroll
-                for (int t = 0; t < V / 2; ++t) held[i].w[t] = 0u;
-            }
+            held[i] = zero_row_vec<V>();
+            if (g < groups) held[i] = load_row_vec<V>(row, g);
         }
         if (MODE != 2) {
 #pragma unroll
-            for (int i = 0; i < G; ++i) mx = qvec_max_bits<V>(held[i], mx);
+            for (int i = 0; i < G; ++i) mx = max_pairs<V>(held[i], mx);
         }
     } else if (MODE != 2) {
-        for (int64_t g = lr; g < groups; g += kStride) mx = qvec_max_bits<V>(load_qvec<V>(row, g), mx);
+        for (int64_t g = lr; g < groups; g += kStride) mx = max_pairs<V>(load_row_vec<V>(row, g), mx);
     }
     float a = 0.0f;
     if constexpr (MODE == 2) {
         if (live) a = a_scale[m];
     } else {
-        mx = wave_max_u32(mx);
+        mx = wave_max_u32(max_of_pair(mx));
         if constexpr (WPR > 1) {
             if ((threadIdx.x & 63) == 0) s_max[wave] = mx;
             __syncthreads();
@@ -208,44 +176,15 @@ __global__ __launch_bounds__(256) void quant_act_kernel(const uint16_t* __restri
         if (live && lr == 0) a_scale[m] = a;
     }
 
-    // V codes per group: one word (V = 4) or two (V = 8)
-    auto quantv = [&](const QVec<V>& v, uint32_t (&packed)[V / 4]) {
-#pragma unroll
-        for (int w = 0; w < V / 4; ++w) {
-            const uint32_t h[4] = {v.w[2 * w] & 0xFFFFu, v.w[2 * w] >> 16, v.w[2 * w + 1] & 0xFFFFu,
-                                   v.w[2 * w + 1] >> 16};
-            uint32_t p = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float r = rintf(bf16_bits_to_f32(h[j]) * a);
-                r = fminf(fmaxf(r, -127.0f), 127.0f);
-                p |= ((uint32_t)(int)r & 0xFFu) << (8 * j);
-            }
-            packed[w] = p;
-        }
-    };
-    auto store = [&](int64_t g, const uint32_t (&packed)[V / 4]) {
-        if constexpr (V == 8)
-            reinterpret_cast<uint2*>(xq + m * K)[g] = make_uint2(packed[0], packed[1]);
-        else
-            reinterpret_cast<uint32_t*>(xq + m * K)[g] = packed[0];
-    };
     if (G > 0) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             const int64_t g = lr + (int64_t)i * kStride;
-            if (g < groups) {
-                uint32_t packed[V / 4];
-                quantv(held[i], packed);
-                store(g, packed);
-            }
+            if (g < groups) store_codes<V, true>(xq + m * K, g, held[i], a);
         }
     } else {
-        for (int64_t g = lr; g < groups; g += kStride) {
-            uint32_t packed[V / 4];
-            quantv(load_qvec<V>(row, g), packed);
-            store(g, packed);
-        }
+        for (int64_t g = lr; g < groups; g += kStride)
+            store_codes<V, true>(xq + m * K, g, load_row_vec<V>(row, g), a);
     }
 }
 

@@ -1,6 +1,8 @@
-// rows.hpp -- helpers of the kernels that work on whole rows (layer norm, SwiGLU): groups
+// rows.hpp -- helpers of the kernels that work on whole rows (quantization, layer norm, SwiGLU): groups
 // of V bf16 elements, reductions over the waves of one row, int8 codes and their scales.
 #pragma once
+
+#include <type_traits>
 
 #include "device_common.hpp"
 
@@ -106,6 +108,15 @@ __device__ __forceinline__ float pow2_scale(uint32_t amax_bits) {
     return __uint_as_float((uint32_t)(127 + p) << 23);
 }
 
+// f(whether codes of rows with this max |x|, the same in every lane, need the clamp).
+template <class F>
+__device__ __forceinline__ void with_clamp(uint32_t amax_bits, const F& f) {
+    if (__builtin_amdgcn_readfirstlane(amax_bits) >= 0x7F80u)
+        f(std::true_type());
+    else
+        f(std::false_type());
+}
+
 // Activation scale of a row whose max |x| has these bf16 bits: 127 / max(amax, 1e-5), or
 // the power of two above.
 __device__ __forceinline__ float scale_of(uint32_t amax_bits, bool pow2) {
@@ -115,20 +126,24 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits, bool pow2) {
     return 127.0f / amax;
 }
 
-// rne(x * a) of V elements as int8: adding 1.5 * 2^23 to fl(x * a) rounds it to an integer,
-// ties to even, and the sum's low byte is that integer.  The clamp to +-127 never binds:
-// |fl(x * a)| <= 127 (1 + 2^-23) < 127.5 for both kinds of scale.
-template <int V>
+// rne(x * a) of V elements as int8, every code of the library: adding 1.5 * 2^23 to fl(x * a)
+// rounds it to an integer, ties to even, and the sum's low byte is that integer.  Finite rows
+// need no clamp, |fl(x * a)| <= 127 (1 + 2^-23) < 127.5 for both kinds of scale; an infinity
+// becomes +-127 (and, restored by the scale 2^-122 of such a row, infinite again), NaN -127.
+// CLAMP may be false for finite rows (for every row it costs SwiGLU 4096 x 28672 170 -> 179 us).
+template <int V, bool CLAMP>
 __device__ __forceinline__ void store_codes(int8_t* row, int64_t g, const RowVec<V>& v, float a) {
     constexpr float kMagic = 12582912.0f;
     float f[V];
     to_f32<V>(v, f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = CLAMP ? __builtin_amdgcn_fmed3f(f[j] * a, -127.0f, 127.0f) : f[j] * a;
     uint32_t p[V / 4];
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
         uint32_t q[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(f[4 * i + j] * a + kMagic);
+        for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(f[4 * i + j] + kMagic);
         p[i] = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400u) | __builtin_amdgcn_perm(q[3], q[2], 0x04000c0cu);
     }
     if constexpr (V == 8)

@@ -69,3 +69,59 @@ def test_norm_backward_far_from_zero(K, kind):
         rx, rw, size, sw = norm_back_xh(dy[r], x64[r], w, mean[r], rstd[r])
         close(dx, rx, BF * rx.abs() + (1 + BF) * 80 * U * size + TINY, f"{K} {kind} {rows} dx")
         close(dw, rw, 131 * U * sw + TINY, f"{K} {kind} {rows} dweight")
+
+
+# ---------------------------------------------------------------- values that are not finite
+
+def with_values(M, N, seed):
+    """Rows holding an infinity, a negative one, a NaN, all of them, and the largest number."""
+    x = bf16(M, N, seed=seed)
+    inf = float("inf")
+    for m, values in enumerate(([inf], [-inf], [float("nan")], [inf, -inf, float("nan")], [3.38e38])):
+        x[m, torch.arange(len(values)) * 2 + 1] = torch.tensor(values, dtype=torch.bfloat16, device="cuda")
+    return x
+
+
+@pytest.mark.parametrize("N", [12, 252, 2560, 6912, 33000])
+def test_fused_codes_are_the_separate_ones_where_values_are_not_finite(N):
+    g, u = with_values(7, N, 1), with_values(7, N, 2).flip(0).contiguous()
+    h, (gq, uq, gs, us) = bw.swiglu(g, u, checkpoint=True)
+    same = lambda p, q: torch.equal(p.view(torch.int32), q.view(torch.int32))  # NaN scales too
+    for q, s, t in ((gq, gs, g), (uq, us, u)):
+        q2, s2 = bw.quant_act_pow2(t)
+        assert torch.equal(q, q2) and same(s, s2)
+    for scale, f in (("absmax", bw.quant_act), ("pow2", bw.quant_act_pow2)):
+        hq, hs = bw.swiglu_quant(g, u, scale=scale)
+        q2, s2 = f(h)
+        assert torch.equal(hq, q2) and same(hs, s2), scale
+        x = with_values(7, N, 3)
+        y = bw.layernorm(x)
+        xq, a = bw.layernorm_quant(x, scale=scale)
+        q2, s2 = f(y)
+        assert torch.equal(xq, q2) and same(a, s2), scale
+
+
+@pytest.mark.parametrize("N", [12, 1024, 2560])
+def test_an_infinity_is_not_restored_as_a_number(N):
+    # the largest code times the smallest step: beyond bf16's range again
+    x = with_values(7, N, 4)
+    for q, s in (bw.quant_act_pow2(x), bw.swiglu(x, torch.ones_like(x), checkpoint=True)[1][::2]):
+        back = bw.dequant_act(q, s)
+        assert back[0, 1] == float("inf") and back[1, 1] == -float("inf")
+
+
+def ref_codes(x, a):
+    """The documented order of a code: product, round half even, clamp (NaN: the lower end)."""
+    r = torch.round(x.float() * a[:, None])
+    return torch.where(torch.isnan(r), torch.full_like(r, -127.0), r.clamp(-127, 127)).to(torch.int8)
+
+
+@pytest.mark.parametrize("M,K", [(7, 12), (7, 2560), (600, 1024), (1100, 260), (7, 20004), (2000, 14336)])
+def test_codes_of_both_scales_and_of_the_tensor(M, K):
+    x = with_values(M, K, K)
+    for f in (bw.quant_act, bw.quant_act_pow2, bw.quant_act_per_tensor):
+        q, a = f(x)
+        assert torch.equal(q, ref_codes(x, a)), f.__name__
+        tail = x[5:].clone()
+        q, a = f(tail)
+        assert torch.equal(q, ref_codes(tail, a)) and torch.isfinite(a).all(), f.__name__
