@@ -36,11 +36,11 @@
 //  * Few output tiles: l is also split over blocks (slices); every slice writes fp32 partial
 //    sums to the workspace and a second launch adds them in a fixed order.
 //  * Tails: what lies past the end of l reads as zeros through the buffer descriptors' bounds
-//    or a mask.  Rows that start off a dword are put together from the dwords around them, and
-//    the last of these may hold one value more than the tensor: rows past the end are then
-//    sent out of bounds by their number (a zero in the other operand is not enough, 0 x NaN is
-//    NaN).  Columns past i or j are computed from whatever lies there and never stored (they
-//    only reach their own outputs).
+//    or a mask.  Rows that start off a dword are put together from the dwords around them; the
+//    last of these may hold one value more than the tensor, which must not enter as the start
+//    of the next row (a zero in the other operand is not enough, 0 x NaN is NaN): see Rows.
+//    Columns past i or j are computed from whatever lies there and never stored (they only
+//    reach their own outputs).
 // Measured in one run (bf16 out; beside it a library's bf16 product, 1250 TFLOP/s at 8192^3 and
 // 887 to 935 on transposed left operands like dw's): dx 8192^3 830 us, 1326 TFLOP/s, the matrix
 // cores busy 56% of the cycles at 4096^3 (the chip holds about 1.8 GHz under such a load, where
@@ -72,6 +72,12 @@ typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 
 // high bytes of bf16(2w) by code (w = code - 1): -2, 0, +2, and 0 for the unused code
 constexpr uint32_t kHi2w = 0x004000C0u;
+
+// How the rows of an operand lie.  kOddEnd: kOdd with an odd number of rows in a single column
+// of tiles (MODE 0), where the tile that needs the last row's half dword also has the column
+// that the other half would enter; there the rows past the end are masked by their number.
+// (Masking wherever rows are odd took registers: dw 512 x 6911 x 2560 46 -> 60 us.)
+enum Rows { kWhole, kOdd, kOddEnd };
 
 struct GradArgs {
     const uint16_t* dy[BITNET_MAX_GROUPS];  // MODE 0: (L, I); MODE 1: (I, L[g])
@@ -127,10 +133,11 @@ __device__ __forceinline__ int chunk(int i, int c) {
     return i * (2 * BL) + ((c ^ (CPR == 8 ? (i & 7) : ((i >> 1) & 3))) << 4);
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, int D, int W, bool ALIGNED>
+template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, int D, int W, Rows ROWS>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel(GradArgs p) {
     constexpr int WPG = (BM / WM) * (BN / WN);  // waves of a group
     constexpr int TG = 64 * WPG;                // threads of a group
+    constexpr bool ALIGNED = ROWS == kWhole;
     constexpr int NI = WM / 32, NJ = WN / 32, KS = BL / 16;
     constexpr int kBRow = MODE == 0 ? 2 * BN : BN / 4;   // bytes of a row of B in LDS
     constexpr int kA = BM * BL * 2, kB = kBRow * BL;      // bytes of one stage
@@ -191,8 +198,11 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     const uint8_t *pa, *pb, *ps;
     uint32_t voff_a[NA], voff_b[NB];
     auto padded = [](int l) { return (l + BL - 1) / BL * BL; };
-    // the last element of rows at odd places lies in a dword that the descriptor has to cover
-    auto whole = [](int bytes) { return ALIGNED ? bytes : (bytes + 3) & ~3; };
+    // The last element of rows at odd places may lie in the lower half of a dword.  The
+    // descriptor covers that dword for the tiles that hold the last column; in MODE 0 it ends
+    // before it for the others, of which the first has the column behind the last element.
+    const int up = MODE == 1 || i0 + BM >= I ? 3 : 0;
+    auto whole = [&](int bytes) { return ALIGNED ? bytes : (bytes + up) & ~3; };
     auto enter = [&]() {  // at l0 of group q
         const int stop = L < end ? L : end;
         left = stop - l0;
@@ -266,10 +276,12 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     Loads ld[D];
     auto load_a = [&](Loads& v, int n) {
         if constexpr (MODE == 0) {
-            if (ALIGNED)
+            if (ALIGNED) {
                 v.a[n] = load16(ra, voff_a[n]);
-            else  // the rounded descriptor reaches into the row behind the last one
-                v.a[n] = load8_half(ra, (tg + n * TG) / (BM / 8) < left ? voff_a[n] : 0x80000000u, 0);
+            } else {
+                const bool in = ROWS == kOdd || (tg + n * TG) / (BM / 8) < left;
+                v.a[n] = load8_half(ra, in ? voff_a[n] : 0x80000000u, 0);
+            }
         } else {
             if (ALIGNED) {  // whole chunks: those past the row's end read as zeros
                 const bool in = 8 * (tg % (BL / 8)) < left;
@@ -686,17 +698,23 @@ GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
     return best;
 }
 
-template <int C>
-void launch_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
+template <int C, Rows ROWS>
+void launch_rows(const GradArgs& a, hipStream_t stream) {
     constexpr GradCfg k = kCfg[C];
     const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices));
     const dim3 block(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g);
+    hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, ROWS>), grid, block, 0,
+                       stream, a);
+}
+
+template <int C>
+void launch_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
     if (aligned)
-        hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, true>), grid,
-                           block, 0, stream, a);
+        launch_rows<C, kWhole>(a, stream);
+    else if (kCfg[C].mode == 0 && a.tiles_i == 1 && a.L[0] % 2 != 0)
+        launch_rows<C, kCfg[C].mode == 0 ? kOddEnd : kOdd>(a, stream);
     else
-        hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, false>), grid,
-                           block, 0, stream, a);
+        launch_rows<C, kOdd>(a, stream);
 }
 
 template <size_t... C>

@@ -14,6 +14,7 @@ pytestmark = pytest.mark.gpu
 
 # odd tokens and odd rows: the last value of dy shares its dword with what lies behind it
 @pytest.mark.parametrize("M,N,K", [(1, 1, 4), (3, 17, 20), (31, 63, 252), (33, 65, 260), (129, 641, 2564),
+                                   (65, 127, 260), (97, 129, 516), (7, 255, 16384), (9, 257, 16384),
                                    (1001, 641, 2560), (2047, 4097, 14340)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_grad_weight_of_a_prefix(M, N, K, dt):
