@@ -481,7 +481,9 @@ int bitnet_grad_input(int64_t M, int64_t K, int64_t groups, const uint16_t* cons
  *   dy         : bf16 (M, N), N <= BITNET_MAX_K, M <= BITNET_GRAD_MAX_M.
  *   xq, a_scale: int8 (M, K) and float (M), positive.  Each xq * (1 / a) is rounded to bf16
  *                once; it is exact for power-of-two scales (bitnet_quant_act_pow2), and then
- *                only the fp32 sum and the output round.
+ *                only the fp32 sum and the output round.  A scale of NaN (of a token with a NaN)
+ *                makes all of dw NaN; under a scale of 0 (of one with an infinity, from
+ *                bitnet_quant_act) the infinity's code of +-127 is infinite again.
  *   dw         : (N, K), BITNET_OUT_F32 or BITNET_OUT_BF16.
  *   workspace  : as in bitnet_grad_input.
  */

@@ -338,9 +338,11 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
             if (h < 0) {
                 // 1 / a: the reciprocal (1 ulp) and one Newton step, which leaves 2^-46 before its
                 // rounding and keeps powers of two exact, in a third of a division's
-                // instructions.  Rows past the end: scale 0.
-                const float a = v.s[n], r = __builtin_amdgcn_rcpf(a);
-                inv = a > 0.0f ? __builtin_fmaf(__builtin_fmaf(-a, r, 1.0f), r, r) : 0.0f;
+                // instructions.  NaN, the scale of a token with a NaN, stays NaN; 0, of one with
+                // an infinity, gives 2^127, under which the infinity's code of +-127 is infinite
+                // and zeros stay zeros: rows past the end have this scale and only zeros.
+                const float a = v.s[n], r = __builtin_fminf(__builtin_amdgcn_rcpf(a), 0x1p126f);
+                inv = __builtin_fmaf(__builtin_fmaf(-a, r, 1.0f), r, r);
             } else {
                 // each value rounded once (not at all for a power of two)
                 const uint32_t u = v.b[n][h >> 1];

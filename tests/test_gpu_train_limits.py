@@ -126,3 +126,22 @@ def test_codes_of_both_scales_and_of_the_tensor(M, K):
         tail = x[5:].clone()
         q, a = f(tail)
         assert torch.equal(q, ref_codes(tail, a)) and torch.isfinite(a).all(), f.__name__
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 16, 64), (33, 65, 260), (512, 2560, 2560), (2048, 4096, 14336)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_weight_gradient_shows_a_token_that_is_not_finite(M, N, K, value):
+    # the absmax scale of a token with a NaN is NaN, with an infinity 0: neither may pass
+    # for a token of zeros
+    dy = bf16(M, N, seed=1, scale=1e-3, hot=False)
+    dy[M - 1] = 1e-3
+    x = bf16(M, K, seed=2)
+    x[M - 1, ::7] = value
+    xq, a = bw.quant_act(x)
+    dw = bw.grad_weight(dy, xq, a)
+    seen = torch.arange(K, device="cuda") % 7 == 0
+    if value == float("inf"):
+        assert a[M - 1] == 0
+        assert torch.isinf(dw[:, seen]).all() and torch.isfinite(dw[:, ~seen]).all()
+    else:
+        assert torch.isnan(a[M - 1]) and torch.isnan(dw).all()
