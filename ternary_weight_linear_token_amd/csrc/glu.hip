@@ -224,17 +224,30 @@ hipError_t launch_swiglu_back(const uint16_t* dh, const void* g, const float* g_
                               const float* u_scale, int64_t M, int64_t N, uint16_t* dg, uint16_t* du,
                               hipStream_t stream) {
     const int64_t groups = N / (N % 8 == 0 ? 8 : 4), bpr = (groups + 255) / 256;
-    if (M * bpr > INT32_MAX) return hipErrorInvalidValue;
-    const GluBackArgs a = {dh, g, u, g_scale, u_scale, groups, bpr, dg, du};
-    const dim3 grid((unsigned)(M * bpr)), block(256);
-    if (N % 8 == 0) {
-        if (g_scale) hipLaunchKernelGGL((swiglu_back_kernel<8, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((swiglu_back_kernel<8, false>), grid, block, 0, stream, a);
-    } else {
-        if (g_scale) hipLaunchKernelGGL((swiglu_back_kernel<4, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((swiglu_back_kernel<4, false>), grid, block, 0, stream, a);
+    const int64_t step = max_blocks(256) / bpr;  // rows of a launch
+    const int64_t size = g_scale ? 1 : 2;        // bytes of an element of g and u
+    for (int64_t m = 0; m < M; m += step) {
+        const GluBackArgs a = {dh + m * N,
+                               static_cast<const uint8_t*>(g) + m * N * size,
+                               static_cast<const uint8_t*>(u) + m * N * size,
+                               g_scale ? g_scale + m : nullptr,
+                               u_scale ? u_scale + m : nullptr,
+                               groups,
+                               bpr,
+                               dg + m * N,
+                               du + m * N};
+        const dim3 grid((unsigned)((M - m < step ? M - m : step) * bpr)), block(256);
+        if (N % 8 == 0) {
+            if (g_scale) hipLaunchKernelGGL((swiglu_back_kernel<8, true>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((swiglu_back_kernel<8, false>), grid, block, 0, stream, a);
+        } else {
+            if (g_scale) hipLaunchKernelGGL((swiglu_back_kernel<4, true>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((swiglu_back_kernel<4, false>), grid, block, 0, stream, a);
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 }  // namespace bitnet

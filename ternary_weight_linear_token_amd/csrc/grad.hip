@@ -731,7 +731,8 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
     if ((size_t)pl.slices * n * 4 > ws_bytes) pl.slices = 1;
     const GradCfg& k = kCfg[pl.cfg];
     const int64_t ti = (a.I + k.bm - 1) / k.bm, tj = (a.J + k.bn - 1) / k.bn;
-    if (ti * tj * pl.slices > INT32_MAX / 8) return hipErrorInvalidValue;
+    // (millions of tokens make 256 x 256 tiles, so that what fits the card fits a launch)
+    if (ti * tj * pl.slices > max_blocks(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g)) return hipErrorInvalidValue;
     a.tiles_i = (int)ti;
     a.tiles_j = (int)tj;
     a.steps = pl.steps;

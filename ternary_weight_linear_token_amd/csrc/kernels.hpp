@@ -9,6 +9,10 @@
 
 namespace bitnet {
 
+// A launch has fewer than 2^32 threads along x; longer problems take several launches of at
+// most this many blocks.
+constexpr int64_t max_blocks(int threads) { return ((int64_t)1 << 32) / threads - 1; }
+
 hipError_t launch_pack_weights(const float* w, int64_t N, int64_t K, uint8_t* packed,
                                float* scale, hipStream_t stream);
 hipError_t launch_unpack_weights(const uint8_t* packed, int64_t N, int64_t K, int8_t* codes,

@@ -643,15 +643,22 @@ hipError_t launch_dequant_act(const int8_t* xq, const float* a_scale, int64_t M,
                               hipStream_t stream) {
     const int V = K % 16 == 0 ? 16 : (K % 8 == 0 ? 8 : 4);
     const int64_t groups = K / V, bpr = (groups + 255) / 256;
-    if (M * bpr > INT32_MAX) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(M * bpr)), block(256);
-    if (V == 16)
-        hipLaunchKernelGGL(dequant_kernel<16>, grid, block, 0, stream, xq, a_scale, groups, bpr, x);
-    else if (V == 8)
-        hipLaunchKernelGGL(dequant_kernel<8>, grid, block, 0, stream, xq, a_scale, groups, bpr, x);
-    else
-        hipLaunchKernelGGL(dequant_kernel<4>, grid, block, 0, stream, xq, a_scale, groups, bpr, x);
-    return hipGetLastError();
+    const int64_t step = max_blocks(256) / bpr;  // rows of a launch
+    for (int64_t m = 0; m < M; m += step) {
+        const dim3 grid((unsigned)((M - m < step ? M - m : step) * bpr)), block(256);
+        const int8_t* const q = xq + m * K;
+        const float* const a = a_scale + m;
+        uint16_t* const out = x + m * K;
+        if (V == 16)
+            hipLaunchKernelGGL(dequant_kernel<16>, grid, block, 0, stream, q, a, groups, bpr, out);
+        else if (V == 8)
+            hipLaunchKernelGGL(dequant_kernel<8>, grid, block, 0, stream, q, a, groups, bpr, out);
+        else
+            hipLaunchKernelGGL(dequant_kernel<4>, grid, block, 0, stream, q, a, groups, bpr, out);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace bitnet

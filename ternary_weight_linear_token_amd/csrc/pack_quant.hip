@@ -308,8 +308,15 @@ hipError_t launch_quant_rows_v(const uint16_t* x, int64_t M, int64_t K, int8_t* 
 template <int MODE>
 hipError_t launch_quant_rows(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, float* a_scale,
                              hipStream_t stream) {
-    if (K % 8 == 0) return launch_quant_rows_v<MODE, 8>(x, M, K, xq, a_scale, stream);
-    return launch_quant_rows_v<MODE, 4>(x, M, K, xq, a_scale, stream);
+    const int64_t step = max_blocks(256);  // rows of a launch, a block has at least one
+    for (int64_t m = 0; m < M; m += step) {
+        const int64_t n = M - m < step ? M - m : step;
+        const hipError_t e = K % 8 == 0
+            ? launch_quant_rows_v<MODE, 8>(x + m * K, n, K, xq + m * K, a_scale + m, stream)
+            : launch_quant_rows_v<MODE, 4>(x + m * K, n, K, xq + m * K, a_scale + m, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_quant_act(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, float* a_scale,

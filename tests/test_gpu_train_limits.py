@@ -145,3 +145,47 @@ def test_weight_gradient_shows_a_token_that_is_not_finite(M, N, K, value):
         assert torch.isinf(dw[:, seen]).all() and torch.isfinite(dw[:, ~seen]).all()
     else:
         assert torch.isnan(a[M - 1]) and torch.isnan(dw).all()
+
+
+# ------------------------------------------------------------------- more rows than one launch
+
+def in_parts(f, args, rows):
+    """f over blocks of rows, joined."""
+    outs = [f(*[a[i: i + rows] for a in args]) for i in range(0, args[0].shape[0], rows)]
+    return [torch.cat(p) for p in zip(*[o if isinstance(o, tuple) else (o,) for o in outs])]
+
+
+def noise(M, K, seed):
+    """bf16 rows of any size, quickly: bits of a counter scrambled, exponents near 1."""
+    i = torch.arange(M * K, dtype=torch.int32, device="cuda").mul_(-1640531527).add_(seed)
+    return ((i >> 16).to(torch.int16) & -28673 | 0x3000).view(torch.bfloat16).view(M, K)
+
+
+# 2^32 threads are the limit of a launch: 2^24 blocks of 256
+@pytest.mark.parametrize("K", [4, 8])
+def test_rows_past_one_launch(K):
+    M, part = (1 << 24) + 1029, 1 << 22
+    x, u, dh = noise(M, K, 1), noise(M, K, 2), noise(M, K, 3)
+    q, a = bw.quant_act_pow2(x)
+    assert torch.equal(bw.dequant_act(q, a), in_parts(bw.dequant_act, (q, a), part)[0])
+    dg, du = bw.swiglu_backward(dh, x, u)
+    for got, want in zip((dg, du), in_parts(bw.swiglu_backward, (dh, x, u), part)):
+        assert torch.equal(got, want)
+    uq, us = bw.quant_act_pow2(u)
+    dg, du = bw.swiglu_backward(dh, q, uq, a, us)
+    for got, want in zip((dg, du), in_parts(bw.swiglu_backward, (dh, q, uq, a, us), part)):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("f", [bw.quant_act, bw.quant_act_pow2, bw.quant_act_per_tensor])
+def test_quantized_rows_past_one_launch(f):
+    # four rows a block
+    M, K = (1 << 26) + 1029, 4
+    x = noise(M, K, 5)
+    q, a = f(x)
+    if f is bw.quant_act_per_tensor:
+        scale = torch.tensor(127.0) / x.float().abs().max().cpu()  # divided on the CPU, rounded once
+        assert torch.equal(a, scale.cuda().expand(M)) and torch.equal(q, ref_codes(x, a))
+    else:
+        want = in_parts(f, (x,), 1 << 24)
+        assert torch.equal(q, want[0]) and torch.equal(a, want[1])
