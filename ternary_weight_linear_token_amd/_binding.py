@@ -486,6 +486,10 @@ def bitlinear(x, packed, w_scale, out_dtype="f32"):
 
 
 # ------------------------------------------------------------ the training side of a layer
+#
+# These functions are the two passes themselves and record no graph.  A tensor that requires
+# grad is refused while grad mode is on, where its gradient would end without a word; inside
+# the forward and backward of a torch.autograd.Function, and under torch.no_grad(), it is off.
 
 SCALE_ABSMAX, SCALE_POW2 = 0, 1
 _SCALE_NAMES = {"absmax": SCALE_ABSMAX, "pow2": SCALE_POW2}
@@ -500,11 +504,14 @@ def _arg(t, dtype, name, shape, device):
     if t is None:
         return None
     if type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous() and (
-            shape is None or t.shape == shape):
+            shape is None or t.shape == shape) and not t.requires_grad:
         return t.data_ptr()
     ptr = _tensor(t, dtype, name, shape)  # raises what is wrong, or takes a subclass
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad, but the result records no graph: call this in a "
+                         "torch.autograd.Function, under torch.no_grad() or on a detached tensor")
     return ptr
 
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import ternary_weight_linear_token_amd as bw
-from test_gpu_train import BF, TINY, U, bf16, close, f32
+from test_gpu_train import BF, TINY, U, bf16, close, f32, ternary
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +189,64 @@ def test_quantized_rows_past_one_launch(f):
     else:
         want = in_parts(f, (x,), 1 << 24)
         assert torch.equal(q, want[0]) and torch.equal(a, want[1])
+
+
+# ----------------------------------------------------------------- automatic differentiation
+
+def test_inputs_that_want_a_gradient_are_refused():
+    # the results carry no graph: a gradient would stop here without a word
+    M, K, N = 4, 64, 16
+    x, q = bf16(M, K, seed=1), torch.ones((M, K), dtype=torch.int8, device="cuda")
+    dy, s = bf16(M, N, seed=2), torch.ones(M, device="cuda")
+    w, (p, ws) = torch.ones(K, device="cuda"), ternary(N, K)
+    want = lambda t: t.clone().requires_grad_()
+    calls = [
+        (lambda: bw.quant_act_pow2(want(x)), lambda: bw.quant_act_pow2(x)),
+        (lambda: bw.dequant_act(q, want(s)), lambda: bw.dequant_act(q, s)),
+        (lambda: bw.layernorm(want(x)), lambda: bw.layernorm(x)),
+        (lambda: bw.layernorm(x, want(w)), lambda: bw.layernorm(x, w)),
+        (lambda: bw.layernorm(x, torch.nn.Parameter(w), w), lambda: bw.layernorm(x, w, w)),
+        (lambda: bw.layernorm_quant(x, w, want(w)), lambda: bw.layernorm_quant(x, w, w)),
+        (lambda: bw.layernorm_backward(x, want(x), w, s, s), lambda: bw.layernorm_backward(x, x, w, s, s)),
+        (lambda: bw.swiglu(want(x), x), lambda: bw.swiglu(x, x)),
+        (lambda: bw.swiglu_quant(x, want(x)), lambda: bw.swiglu_quant(x, x)),
+        (lambda: bw.swiglu_backward(want(x), x, x), lambda: bw.swiglu_backward(x, x, x)),
+        (lambda: bw.grad_input(want(dy), p, ws), lambda: bw.grad_input(dy, p, ws)),
+        (lambda: bw.grad_weight(want(dy), q, s), lambda: bw.grad_weight(dy, q, s)),
+        (lambda: bw.bitlinear_backward(dy, q, s, p, want(ws)),
+         lambda: bw.bitlinear_backward(dy, q, s, p, ws)),
+    ]
+    flat = lambda r: [r] if isinstance(r, torch.Tensor) else [
+        t for v in r if v is not None for t in flat(v)]
+    for bad, good in calls:
+        with pytest.raises(ValueError, match="requires grad"):
+            bad()
+        with torch.no_grad():
+            got = flat(bad())
+        want_bits = flat(good())
+        assert len(got) == len(want_bits) and all(torch.equal(g, r) for g, r in zip(got, want_bits))
+
+
+def test_as_functions_of_automatic_differentiation():
+    # the calls as a user wraps them: both passes of a Function run without a graph
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, b):
+            y, mean, rstd = bw.layernorm(x, w, b, return_stats=True)
+            ctx.save_for_backward(x, w, mean, rstd)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            return bw.layernorm_backward(dy.contiguous(), *ctx.saved_tensors)
+
+    K = 260
+    x, dy = bf16(9, K, seed=1), bf16(9, K, seed=2)
+    w, b = f32(K, seed=3, shift=1.0), f32(K, seed=4)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b)]
+    y = Norm.apply(*leaves)
+    y.backward(dy)
+    y0, mean, rstd = bw.layernorm(x, w, b, return_stats=True)
+    assert torch.equal(y, y0)
+    for leaf, g in zip(leaves, bw.layernorm_backward(dy, x, w, mean, rstd)):
+        assert torch.equal(leaf.grad, g)
