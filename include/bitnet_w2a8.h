@@ -500,6 +500,12 @@ int bitnet_grad_weight(const uint16_t* dy, const int8_t* xq, const float* a_scal
  */
 int bitnet_grad_plan(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N,
                      int32_t* plan);
+/*
+ * bitnet_grad_plan_step -- step : HOST int32 output = values of the sum that a group of waves
+ * takes at a time under that plan (two plans may have the same tile).  Host-only.
+ */
+int bitnet_grad_plan_step(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N,
+                          int32_t* step);
 
 #ifdef __cplusplus
 }

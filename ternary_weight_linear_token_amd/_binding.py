@@ -90,6 +90,7 @@ def lib():
             "bitnet_grad_input_workspace_size": ([i64, i64, i64, p], ctypes.c_size_t),
             "bitnet_grad_input": ([i64, i64, i64, p, p, p, p, p, p, ctypes.c_size_t, p], i32),
             "bitnet_grad_plan": ([i32, i64, i64, i64, p, p], i32),
+            "bitnet_grad_plan_step": ([i32, i64, i64, i64, p, p], i32),
             "bitnet_grad_weight_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
             "bitnet_grad_weight": ([p, p, p, i64, i64, i64, p, i32, p, ctypes.c_size_t, p], i32),
         }
@@ -760,6 +761,16 @@ def grad_plan(M, K, Ns, weight=False):
     out = (ctypes.c_int32 * 4)()
     _check(lib().bitnet_grad_plan(int(weight), int(M), int(K), G, NN, out), "bitnet_grad_plan")
     return tuple(int(v) for v in out)
+
+
+def grad_plan_step(M, K, Ns, weight=False):
+    """Values of the sum per step of the plan that grad_plan gives; host-only."""
+    G = len(Ns)
+    NN = (ctypes.c_int64 * max(G, 1))(*[int(n) for n in Ns])
+    out = ctypes.c_int32()
+    _check(lib().bitnet_grad_plan_step(int(weight), int(M), int(K), G, NN, ctypes.byref(out)),
+           "bitnet_grad_plan_step")
+    return int(out.value)
 
 
 def bitlinear_backward(dy, xq, a_scale, packed, w_scale, dw_dtype="f32"):

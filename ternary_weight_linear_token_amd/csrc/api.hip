@@ -601,18 +601,28 @@ int bitnet_grad_input(int64_t M, int64_t K, int64_t groups, const uint16_t* cons
                                                 workspace, ws_bytes, as_stream(stream)));
 }
 
-int bitnet_grad_plan(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N,
-                     int32_t* plan) {
+static int grad_plan(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N, int first,
+                     int last, int32_t* out) {
     const int st = check_grad_groups(M, K, groups, N);
     if (st) return st;
-    if (!plan || M < 1 || (weight && (groups != 1 || N[0] < 1))) return BITNET_ERR_INVALID_ARG;
-    int p[4];
+    if (!out || M < 1 || (weight && (groups != 1 || N[0] < 1))) return BITNET_ERR_INVALID_ARG;
+    int p[5];
     if (weight)
         bitnet::grad_plan(0, N[0], K, &M, 1, p);
     else
         bitnet::grad_plan(1, M, K, N, (int)groups, p);
-    for (int i = 0; i < 4; ++i) plan[i] = p[i];
+    for (int i = first; i <= last; ++i) out[i - first] = p[i];
     return BITNET_OK;
+}
+
+int bitnet_grad_plan(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N,
+                     int32_t* plan) {
+    return grad_plan(weight, M, K, groups, N, 0, 3, plan);
+}
+
+int bitnet_grad_plan_step(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N,
+                          int32_t* step) {
+    return grad_plan(weight, M, K, groups, N, 4, 4, step);
 }
 
 size_t bitnet_grad_weight_workspace_size(int64_t M, int64_t N, int64_t K) {

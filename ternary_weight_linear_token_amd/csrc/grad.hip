@@ -755,6 +755,7 @@ void grad_plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups, int
     out[1] = k.bn;
     out[2] = k.g;
     out[3] = pl.slices;
+    out[4] = k.bl;
 }
 
 size_t grad_input_workspace_size(int64_t M, int64_t K, int groups, const int64_t* N) {

@@ -127,7 +127,8 @@ hipError_t launch_swiglu_back(const uint16_t* dh, const void* g, const float* g_
 
 // Gradients of the product: dx (M, K) bf16 from `groups` products that share their input, and
 // dw (N, K) fp32 or bf16.  Workspace optional (fp32 partials of a split contraction).
-// grad_plan: out[0..3] = tile rows, tile columns, k-groups, slices of a call with its workspace
+// grad_plan: out[0..4] = tile rows, tile columns, k-groups, slices, values of the sum per step
+// of a call with its workspace
 // (mode 0: dw, I x J = N x K over L[0] = M; mode 1: dx, I x J = M x K over the L[g] = N[g]).
 void grad_plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups, int* out);
 size_t grad_input_workspace_size(int64_t M, int64_t K, int groups, const int64_t* N);

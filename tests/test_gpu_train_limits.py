@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import ternary_weight_linear_token_amd as bw
-from test_gpu_train import BF, TINY, U, bf16, close, f32, ternary
+from test_gpu_train import (BF, TINY, U, bf16, check_grad_input, check_grad_weight, close, f32,
+                            ternary)
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +251,37 @@ def test_as_functions_of_automatic_differentiation():
     assert torch.equal(y, y0)
     for leaf, g in zip(leaves, bw.layernorm_backward(dy, x, w, mean, rstd)):
         assert torch.equal(leaf.grad, g)
+
+
+# ------------------------------------------------------------------ every compiled gradient kernel
+
+# (M, K, Ns) and (M, N, K): each tile, with whole rows, odd ones and (dw) odd ends in a single
+# column of tiles; all of these split the sum, and run unsplit without their workspace.
+# test_train_plans.py holds the list against the plans and the table of tiles.
+DX_TILES = [(1, 176, [1248]), (1, 136, [1347]), (33, 4912, [10120]), (36, 1436, [24747]), (1636, 592, [8784]),
+            (4271, 148, [4456]), (199, 19696, [2368]), (4637, 156, [7698])]
+DW_TILES = [(334, 60, 144), (478, 63, 136), (401, 65, 144), (1909, 60, 148), (2032, 65, 200), (3249, 67, 144),
+            (2956, 134, 11200), (2069, 18479, 148), (3441, 143, 12168)]
+
+
+@pytest.mark.parametrize("M,K,Ns", DX_TILES + [(520, 2052, [4097]), (2048, 4096, [1000, 3001])])
+def test_input_gradient_of_every_kernel(M, K, Ns):
+    big = [bf16(M + 1, n, seed=n + i, scale=1e-3, hot=False) for i, n in enumerate(Ns)]
+    packs, scales = zip(*[ternary(n, K, seed=n + i) for i, n in enumerate(Ns)])
+    for t in big:
+        t[M] = float("nan")  # behind the rows
+    dys = [t[:M] for t in big]
+    for workspace in (None, False):
+        got = bw.grad_input_grouped(dys, packs, scales, workspace=workspace)
+        check_grad_input(dys, packs, scales, K, got, f"{M} {K} {Ns} {workspace}")
+
+
+@pytest.mark.parametrize("M,N,K", DW_TILES + [(2048, 4096, 14336), (2047, 4097, 14340)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_weight_gradient_of_every_kernel(M, N, K, dt):
+    big = bf16(M + 1, N, seed=N, scale=1e-3, hot=False)
+    big[M] = float("nan")
+    xq, a = bw.quant_act_pow2(bf16(M, K, seed=K))
+    for workspace in (None, False):
+        got = bw.grad_weight(big[:M], xq, a, out_dtype=dt, workspace=workspace)
+        check_grad_weight(big[:M], xq, a, dt, got, f"{M} {N} {K} {dt} {workspace}")
