@@ -463,7 +463,8 @@ int bitnet_swiglu_backward(const uint16_t* dh, const void* g, const float* g_sca
  *   dy, packed, w_scale, N : HOST arrays of `groups` entries, read during the call only: bf16
  *                (M, N[g]), uint8 (N[g], K/4), float (N[g]) device pointers.  N[g] == 0 adds
  *                nothing; N[g] <= BITNET_MAX_K, M <= BITNET_GRAD_MAX_M.  An unused code 0b11
- *                counts as weight 0.
+ *                counts as weight 0 (the int8 products read it as +2: such weights have to go
+ *                through bitnet_repack_codes before either).
  *   dx         : bf16 (M, K).  Each dy * w_scale is rounded to bf16 once, products with w and
  *                their sum are fp32, and the sum over all groups is rounded once.
  *   workspace  : optional scratch: with bitnet_grad_input_workspace_size bytes the sum is split

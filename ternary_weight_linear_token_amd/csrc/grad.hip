@@ -648,18 +648,21 @@ struct GradCfg {
     double base, step_alone, step_full;
 };
 constexpr GradCfg kCfg[] = {
-    // weight gradient (times and costs taken before the epilogue lost its branches, which takes
-    // 10 to 15% off all three).  256 x 256 is the fastest per flop (2048 x 4096 x 14336: 262 us,
-    // 128 x 128 tiles 305); its 256 blocks at a time leave most of the chip idle in a short last
-    // round (512 x 6912 x 2560, 270 tiles: 53 us), which 128 x 128 tiles, two or four blocks per
-    // CU, fill better (45 and 43 us); four share a CU only at half the rows per step.
+    // weight gradient.  256 x 256 is the fastest per flop (2048 x 4096 x 14336: 232 us, 128 x 128
+    // tiles 278 and 284); its 256 blocks at a time leave most of the chip idle in a short last
+    // round (2048 x 6912 x 2560, 270 tiles: 107 us), which 128 x 128 tiles, two or four blocks
+    // per CU, fill better (96 and 109; of 512 tokens 33 and 35 against 40); four share a CU only
+    // at half the rows per step.  The costs below are from before the epilogue lost its
+    // branches, 10 to 15% too high alike; the tile they pick was within 8% of the best of the
+    // three at six sizes measured since.
     {0, 256, 256, 128, 64, 1, 64, 1, 1, 1, 13, 1.8, 1.8},
     {0, 128, 128, 64, 64, 1, 64, 1, 1, 2, 8, 0.73, 1.15},
     {0, 128, 128, 64, 64, 1, 32, 1, 4, 4, 8, 0.43, 1.25},
-    // input gradient.  256 x 256 for the largest (2048 x 28672 x 4096: 406 us, 256 x 128 519);
-    // 256 x 128 where that makes one round of the chip (2048 x 4096 x 4096: 75 us against 78);
-    // 64 x 128 with the sum over four groups of waves for hundreds of tokens (512 x 3840 x 2560:
-    // 26 us, 128 x 128 in three slices 29); 32 x 128 below (4 x 2560 x 2560 in slices: 9.5 us).
+    // input gradient.  256 x 256 for the largest (2048 x 28672 x 4096 in two slices: 370 us,
+    // 256 x 128 457); 256 x 128 where that makes one round of the chip (2048 x 4096 x 4096: 72 us
+    // against 77); 64 x 128 with the sum over four groups of waves for hundreds of tokens (512 x
+    // 3840 x 2560: 25 us, 256 x 128 in four slices 33); 32 x 128 below (4 x 2560 x 2560 in ten
+    // slices with the join: 8.4 us).
     {1, 256, 256, 128, 64, 1, 64, 1, 1, 1, 8, 1.7, 1.7},
     {1, 256, 128, 128, 64, 2, 32, 1, 1, 1, 9, 1.0, 1.0},
     {1, 64, 128, 64, 64, 4, 32, 2, 1, 1, 7, 0.59, 0.59},

@@ -285,3 +285,23 @@ def test_weight_gradient_of_every_kernel(M, N, K, dt):
     for workspace in (None, False):
         got = bw.grad_weight(big[:M], xq, a, out_dtype=dt, workspace=workspace)
         check_grad_weight(big[:M], xq, a, dt, got, f"{M} {N} {K} {dt} {workspace}")
+
+
+def test_stream_and_device_getters(monkeypatch):
+    # the short cuts give what torch's public functions give, and those serve in their place
+    from ternary_weight_linear_token_amd import _binding
+    x = bf16(5, 260, seed=1)
+    want = bw.layernorm(x)
+    public_stream = lambda index: torch.cuda.current_stream(index).cuda_stream
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            assert _binding._raw_stream(x.device.index) == stream.cuda_stream == public_stream(x.device.index)
+    assert _binding._raw_device() == torch.cuda.current_device()
+    monkeypatch.setattr(_binding, "_raw_stream", public_stream)
+    monkeypatch.setattr(_binding, "_raw_device", torch.cuda.current_device)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = bw.layernorm(x)
+    side.synchronize()
+    assert torch.equal(got, want)
