@@ -389,8 +389,8 @@ typedef enum {
  * x * a is exact, so xq is the round-half-even of the exact value, and xq / a is exact in
  * bf16: bitnet_grad_weight on such codes has no rounding before its fp32 sum.  The product
  * entry points take these codes like any others.
- * In a row that is not finite every entry point that writes codes gives an infinity the code
- * +-127, which its scale of 2^-122 restores to an infinity, and NaN the code -127.
+ * In a row that is not finite the quantization, norm and SwiGLU entry points alike give an
+ * infinity the code +-127, which the scale of 2^-122 restores to an infinity, and NaN -127.
  */
 int bitnet_quant_act_pow2(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, float* a_scale,
                           void* stream);

@@ -9,8 +9,10 @@
 // a row is held in the registers of WPR waves (up to four groups of V elements of g, u and h
 // per lane), all loads issued together, the maxima of g, u and h reduced behind one barrier;
 // longer rows are read again from cache.  Backward: no row reduction, V elements a thread.
-// Measured, inputs out of cache: 2048 x 14336 forward with checkpoints 40 us, 5.8 TB/s, backward
-// from them 36.5 us, 6.4 TB/s (a copy: 5.3); 32768 x 2560 138 and 137 us, 4.9 TB/s.
+// Measured, inputs out of cache: 2048 x 14336 forward with checkpoints 40 us, 5.9 TB/s, backward
+// from them 36.8 us, 6.4 TB/s, from bf16 43.8 us, 6.7 TB/s (a copy: 5.3); 32768 x 2560 138, 136 and
+// 169 us, 4.9 to 5.0 TB/s; 4096 x 28672 (16 waves, seven registers in scratch) 184, 161 and 203 us,
+// 5.1 to 5.8 TB/s.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "rows.hpp"

@@ -41,16 +41,17 @@
 //    of the next row (a zero in the other operand is not enough, 0 x NaN is NaN): see Rows.
 //    Columns past i or j are computed from whatever lies there and never stored (they only
 //    reach their own outputs).
-// Measured in one run (bf16 out; beside it a library's bf16 product, 1250 TFLOP/s at 8192^3 and
-// 887 to 935 on transposed left operands like dw's): dx 8192^3 830 us, 1326 TFLOP/s, the matrix
-// cores busy 56% of the cycles at 4096^3 (the chip holds about 1.8 GHz under such a load, where
-// the peak is 1.9 PFLOP/s); dw 8192^3 906 us, 1214 TFLOP/s: both operands of dw are read
+// Measured in one run (bf16 out; beside it a library's bf16 product, 1399 TFLOP/s at 8192^3 and
+// 1223 on a transposed left operand like dw's): dx 8192^3 806 us, 1364 TFLOP/s, the matrix cores
+// busy 58% of the cycles at 4096^3 (the chip holds about 1.8 GHz under such a load, where the peak
+// is 1.9 PFLOP/s); dw 8192^3 884 us, 1244 TFLOP/s, busy 55%: both operands of dw are read
 // transposed as bf16, 192 KB of LDS reads a step against 132 KB.  What is left is the vector
 // instructions of the conversion, which the matrix instructions hide in part.
-// One token to dozens: dx 4 x 2560 x 2560 5.7 us and 2.0 to 3.4 for the join, launch and
-// latency; 512 x 3840 x 2560 24 us against 7.3 at the rate of a large product: 160 tiles on 256
-// CUs and a chain of 30 short steps.  dw 512 x 6912 x 2560 fp32 35 us against 16.3 for its
-// 79 MB: 1080 tiles on 1024 places leave a last round of 56.
+// One token to dozens: dx 4 x 2560 x 2560 6.1 us and 3.1 for the join (medians, from HBM), launch
+// and latency; 512 x 3840 x 2560 24 us against 7.3 at the rate of a large product: 160 tiles on
+// 256 CUs, one block on each, and a chain of 30 short steps.  dw 512 x 6912 x 2560 fp32 33 to 36 us
+// against 16.3 for its 79 MB: 1080 tiles on 1024 places leave a last round of 56 (the kernel is
+// held to 128 registers for them and keeps up to six in scratch).
 #include <cmath>
 #include <type_traits>
 #include <utility>

@@ -17,11 +17,14 @@
 // inputs give the same bits).
 //
 // Measured, inputs out of cache (a copy of the same sizes: 5.3 to 5.8 TB/s): forward 8192 x 8192
-// 48.9 us, 5.5 TB/s, with codes instead of y 45.5 us, 4.4 TB/s (the vector instructions of the
+// 45.8 us, 5.9 TB/s, with codes instead of y 42.7 us, 4.7 TB/s (the vector instructions of the
 // statistics and codes, about 290 per 16 columns a lane and row, are then as long as the
-// bytes); backward from a checkpoint 8192 x 4096 42.9 us, 3.9 TB/s, its column sums 4.2 of them;
-// from bf16 65536 x 1024 78 us, 5.2 TB/s; rows over 8192 columns (16 waves, two groups a lane,
-// some registers in scratch) 2.5 TB/s.  One row of 2560: 2.5 us warm, 4.7 cold, latency.
+// bytes); 4096 x 14336 47 us, 5.0 TB/s, with codes 51 us; over 16384 columns the row is read up to
+// four times, 2048 x 28672 57 us, 4.1 TB/s.  Backward from a checkpoint 8192 x 4096 41.2 us, 4.1
+// TB/s, its column sums 4.2 of them; from bf16 65536 x 1024 77 us, 5.2 TB/s; rows over 8192 columns
+// (16 waves, two groups a lane, 24 to 32 registers in scratch) 4096 x 14336 112 us, 3.1 TB/s, and
+// over 16384 (two launches that read everything twice over) 2048 x 28672 162 us, 2.2 TB/s.  One
+// row of 2560: 2.4 us warm, 4.7 cold, latency.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "rows.hpp"
@@ -491,7 +494,7 @@ __global__ __launch_bounds__(1024) void layernorm_join_kernel(const float* __res
 
 // ------------------------------------------------------------------------- dequantize
 // bf16(c * (1 / a)): V codes a thread, blocks of 256 groups along a row.  HBM-bound: 16 codes a
-// thread 8192 x 8192 38 us, 5.3 TB/s (8 codes and a division per value: 49 us).
+// thread 8192 x 8192 34 us, 5.9 TB/s (8 codes and a division per value: 49 us).
 template <int V>
 __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__ xq,
                                                       const float* __restrict__ a_scale, int64_t groups,
