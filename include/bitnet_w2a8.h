@@ -508,6 +508,172 @@ int bitnet_grad_plan(int weight, int64_t M, int64_t K, int64_t groups, const int
 int bitnet_grad_plan_step(int weight, int64_t M, int64_t K, int64_t groups, const int64_t* N,
                           int32_t* step);
 
+/* ==================================================================================
+ * Root-mean-square norm with the residual stream's addition, and the gradients' global norm.
+ * The conventions of the training side above hold.
+ * ================================================================================== */
+
+/*
+ * bitnet_rmsnorm -- root-mean-square norm over K of x, or of the sum of x and a residual, with the
+ * int8 codes of its output fused in.
+ *   s = bf16(x + residual) (or x),  rstd[m] = 1 / sqrt(mean_k s^2 + eps),
+ *   y = s * rstd * weight in fp32, rounded to bf16.
+ *   residual, sum : bf16 (M, K), both or neither; sum receives s and may be x or residual itself
+ *                   (the norm is of the rounded sum: what the next layer and the backward read).
+ *   weight        : float (K), optional (1).   eps: finite, normal, > 0.
+ *   y             : bf16 (M, K), optional.
+ *   xq, a_scale   : int8 (M, K) and float (M), both or neither: bit-identical to
+ *                   bitnet_quant_act (scale = BITNET_SCALE_ABSMAX) or bitnet_quant_act_pow2
+ *                   (BITNET_SCALE_POW2) of the bf16 y.  y or xq is needed.
+ *   rstd          : float (M), optional; the backward takes it.
+ * The mean of squares is an fp32 sum: rows whose squares overflow it (values past 2^63) get rstd 0.
+ */
+int bitnet_rmsnorm(const uint16_t* x, const uint16_t* residual, const float* weight, float eps,
+                   int64_t M, int64_t K, uint16_t* sum, uint16_t* y, int8_t* xq, float* a_scale,
+                   int scale, float* rstd, void* stream);
+
+/*
+ * bitnet_rmsnorm_backward -- with z = x * rstd and g = dy * weight:
+ *   dx = rstd * (g - z * mean_k (g * z)) + dresidual, rounded to bf16 (with a residual in the
+ *   forward it is the gradient of both summands);  dweight[k] = sum_m dy * z (fp32, optional).
+ *   x, x_scale : what was normalized (the forward's sum, or x): bf16 (M, K) with x_scale NULL, or
+ *                the checkpoint: int8 (M, K) codes with their float (M) scales.
+ *   dresidual  : bf16 (M, K), optional: the gradient that reaches the sum along the residual stream.
+ *   weight     : float (K), optional (1).   rstd : of the forward.
+ *   workspace  : with dweight, bitnet_rmsnorm_backward_workspace_size(M, K) bytes of scratch (else
+ *                BITNET_ERR_WORKSPACE); calls that share one must be ordered.
+ */
+size_t bitnet_rmsnorm_backward_workspace_size(int64_t M, int64_t K);
+int bitnet_rmsnorm_backward(const uint16_t* dy, const void* x, const float* x_scale,
+                            const float* weight, const float* rstd, const uint16_t* dresidual,
+                            int64_t M, int64_t K, uint16_t* dx, float* dweight, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * bitnet_grad_norm -- the 2-norm of all values of `count` tensors together.
+ *   grads, n, dtype : HOST arrays of `count` entries, read during the call only: device pointers,
+ *                     numbers of values (0 allowed, then the pointer is not examined) and types
+ *                     (BITNET_OUT_F32 or BITNET_OUT_BF16).  Values need only the alignment of their
+ *                     type.  A tensor that is listed twice counts twice.
+ *   norm            : float (1), 4-byte aligned.  Squares and their sum are fp64 (nothing overflows
+ *                     or vanishes on the way), rounded once; count == 0 gives 0.
+ *   workspace       : bitnet_grad_norm_workspace_size(count) bytes, 16-byte aligned; calls that share
+ *                     one must be ordered.
+ */
+size_t bitnet_grad_norm_workspace_size(int64_t count);
+int bitnet_grad_norm(int64_t count, const void* const* grads, const int64_t* n, const int32_t* dtype,
+                     float* norm, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * bitnet_clip_grads -- scale the tensors so that their norm is at most max_norm:
+ *   c = min(1, max_norm / (norm + 1e-6)) in fp32,  out = grad * c in fp32, rounded to the type.
+ *   grads, n, dtype : as in bitnet_grad_norm.
+ *   out             : HOST array of device pointers; out[i] is grads[i] itself (in place; nothing is
+ *                     written where c is 1) or a buffer that overlaps no other tensor of the call
+ *                     (two overlapping outputs, or an output that overlaps another input, return
+ *                     BITNET_ERR_INVALID_ARG).
+ *   max_norm        : finite, >= 0.
+ *   norm_in         : optional float (1): the norm to go by, e.g. one reduced over several GPUs.
+ *                     NULL: the norm of grads, for which the workspace is needed.
+ *   norm_out        : optional float (1): receives the norm.
+ * A norm that is infinite gives c = 0 (and NaN for infinite values), a norm of NaN makes every
+ * gradient NaN.
+ */
+int bitnet_clip_grads(int64_t count, const void* const* grads, void* const* out, const int64_t* n,
+                      const int32_t* dtype, float max_norm, const float* norm_in, float* norm_out,
+                      void* workspace, size_t ws_bytes, void* stream);
+
+/* ==================================================================================
+ * Mixture of experts: T tokens choose J of E experts each, and every expert has a ternary matrix
+ * of its own for each product.  The P = T * J pairs, sorted by expert, are the rows of the
+ * products: expert e has the rows offsets[e] .. offsets[e + 1] - 1.
+ * The offsets are read on the device: no call waits for the counts.  Offsets that lie outside
+ * 0 .. P or run backwards leave the outputs unspecified, but cause no access out of bounds; rows
+ * that belong to no expert (behind offsets[E]) are left as they were.
+ * ================================================================================== */
+
+#define BITNET_MAX_EXPERTS 1024
+
+/*
+ * bitnet_expert_order -- the stable order of the pairs by expert.
+ *   ids     : int32 (T, J), or int64 with wide != 0: the expert of each choice.  A choice outside
+ *             0 .. E - 1 (e.g. -1 for the padding of a batch) is dropped.  1 <= J <=
+ *             BITNET_MAX_EXPERTS, T * J <= BITNET_GRAD_MAX_M.
+ *   rows    : int32 (T * J): the token of each row; -1 for the rows behind offsets[E].
+ *   offsets : int32 (E + 1).
+ *   slots   : int32 (T, J): the row of each pair, -1 for a dropped one.
+ *   workspace : bitnet_expert_order_workspace_size(T * J, E) bytes (0 for few pairs); calls that
+ *             share one must be ordered.
+ */
+size_t bitnet_expert_order_workspace_size(int64_t P, int64_t E);
+int bitnet_expert_order(const void* ids, int wide, int64_t T, int64_t J, int64_t E, int32_t* rows,
+                        int32_t* offsets, int32_t* slots, void* workspace, size_t ws_bytes,
+                        void* stream);
+
+/*
+ * bitnet_gemm_experts -- bitnet_w2a8_gemm of every expert's rows with its own weights, for up to
+ * BITNET_MAX_GROUPS matrices that read the same activations (gate and up), in one launch.
+ *   xq, a_scale : int8 (T, K) codes and float (T) scales of the tokens.
+ *   rows        : int32 (P): row p reads token rows[p] (a token that is not in 0 .. T - 1 counts as
+ *                 zeros); T * K < 2^31.  NULL: row p reads token p, and T == P.
+ *   offsets     : int32 (E + 1).   P <= BITNET_GRAD_MAX_M, 1 <= E <= BITNET_MAX_EXPERTS.
+ *   packed, w_scale, N, out : HOST arrays of `groups` entries, read during the call only: uint8
+ *                 (E, N[g], K/4), float (E, N[g]), N[g] <= BITNET_MAX_K (0: nothing of that entry is
+ *                 touched), and (P, N[g]) of out_dtype.
+ * Each row is bit-identical to bitnet_w2a8_gemm with BITNET_ALGO_TILED.  Output buffers must not
+ * overlap one another or any input.
+ */
+int bitnet_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T, const int32_t* rows,
+                        const int32_t* offsets, int64_t P, int64_t E, int64_t K, int64_t groups,
+                        const uint8_t* const* packed, const float* const* w_scale, const int64_t* N,
+                        void* const* out, int out_dtype, void* stream);
+
+/*
+ * bitnet_grad_input_experts -- bitnet_grad_input of every expert's rows (without workspace):
+ *   dx[p,k] = sum_g sum_n dy_g[p,n] * w_scale_g[e,n] * w_g[e,n,k], bf16 (P, K), in the rows' order
+ *   (bitnet_combine_experts adds up the rows of a token).
+ *   dy : HOST array of bf16 (P, N[g]) device pointers; packed, w_scale, N as above.
+ */
+int bitnet_grad_input_experts(const int32_t* offsets, int64_t P, int64_t E, int64_t K, int64_t groups,
+                              const uint16_t* const* dy, const uint8_t* const* packed,
+                              const float* const* w_scale, const int64_t* N, uint16_t* dx,
+                              void* stream);
+
+/*
+ * bitnet_grad_weight_experts -- bitnet_grad_weight of every expert's rows (without splitting):
+ *   dw[e,n,k] = sum over the rows p of e of dy[p,n] * xq[t,k] / a_scale[t],  t = rows[p] (or p).
+ *   dy        : bf16 (P, N).   xq, a_scale, T, rows, offsets : as in bitnet_gemm_experts.
+ *   dw        : (E, N, K), BITNET_OUT_F32 or BITNET_OUT_BF16; zeros for an expert without rows.
+ *   workspace : with rows, bitnet_grad_weight_experts_workspace_size(P, K) bytes (the codes in the
+ *               rows' order; else BITNET_ERR_WORKSPACE); calls that share one must be ordered.
+ */
+size_t bitnet_grad_weight_experts_workspace_size(int64_t P, int64_t K);
+int bitnet_grad_weight_experts(const uint16_t* dy, const int8_t* xq, const float* a_scale, int64_t T,
+                               const int32_t* rows, const int32_t* offsets, int64_t P, int64_t E,
+                               int64_t N, int64_t K, void* dw, int out_dtype, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * bitnet_combine_experts -- the weighted sum of a token's rows:
+ *   out[t] = sum_j weights[t,j] * y[slots[t,j]], in fp32, rounded to bf16.
+ *   y       : bf16 (P, D), D % 4 == 0, D <= BITNET_MAX_K.   slots : int32 (T, J), 1 <= J <=
+ *             BITNET_MAX_EXPERTS; a slot outside 0 .. P - 1 adds nothing.
+ *   weights : float (T, J), optional (1).   out : bf16 (T, D).
+ */
+int bitnet_combine_experts(const uint16_t* y, const int32_t* slots, const float* weights, int64_t T,
+                           int64_t J, int64_t P, int64_t D, uint16_t* out, void* stream);
+
+/*
+ * bitnet_combine_experts_backward -- dy[slots[t,j]] = weights[t,j] * dout[t], rounded to bf16, and
+ *   dweights[t,j] = sum_d dout[t,d] * y[slots[t,j],d] in fp32 (0 for a dropped pair).
+ *   dy       : bf16 (P, D); rows that no slot names are left as they were, and no two slots may name
+ *              the same row.
+ *   dweights : float (T, J), optional; y is needed with it alone.   weights : optional (1).
+ */
+int bitnet_combine_experts_backward(const uint16_t* dout, const uint16_t* y, const int32_t* slots,
+                                    const float* weights, int64_t T, int64_t J, int64_t P, int64_t D,
+                                    uint16_t* dy, float* dweights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

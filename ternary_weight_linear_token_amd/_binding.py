@@ -93,6 +93,21 @@ def lib():
             "bitnet_grad_plan_step": ([i32, i64, i64, i64, p, p], i32),
             "bitnet_grad_weight_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
             "bitnet_grad_weight": ([p, p, p, i64, i64, i64, p, i32, p, ctypes.c_size_t, p], i32),
+            "bitnet_rmsnorm": ([p, p, p, ctypes.c_float, i64, i64, p, p, p, p, i32, p, p], i32),
+            "bitnet_rmsnorm_backward_workspace_size": ([i64, i64], ctypes.c_size_t),
+            "bitnet_rmsnorm_backward": ([p, p, p, p, p, p, i64, i64, p, p, p, ctypes.c_size_t, p], i32),
+            "bitnet_grad_norm_workspace_size": ([i64], ctypes.c_size_t),
+            "bitnet_grad_norm": ([i64, p, p, p, p, p, ctypes.c_size_t, p], i32),
+            "bitnet_clip_grads": ([i64, p, p, p, p, ctypes.c_float, p, p, p, ctypes.c_size_t, p], i32),
+            "bitnet_expert_order_workspace_size": ([i64, i64], ctypes.c_size_t),
+            "bitnet_expert_order": ([p, i32, i64, i64, i64, p, p, p, p, ctypes.c_size_t, p], i32),
+            "bitnet_gemm_experts": ([p, p, i64, p, p, i64, i64, i64, i64, p, p, p, p, i32, p], i32),
+            "bitnet_grad_input_experts": ([p, i64, i64, i64, i64, p, p, p, p, p, p], i32),
+            "bitnet_grad_weight_experts_workspace_size": ([i64, i64], ctypes.c_size_t),
+            "bitnet_grad_weight_experts": ([p, p, p, i64, p, p, i64, i64, i64, i64, p, i32, p,
+                                            ctypes.c_size_t, p], i32),
+            "bitnet_combine_experts": ([p, p, p, i64, i64, i64, i64, p, p], i32),
+            "bitnet_combine_experts_backward": ([p, p, p, p, i64, i64, i64, i64, p, p, p], i32),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -778,3 +793,310 @@ def bitlinear_backward(dy, xq, a_scale, packed, w_scale, dw_dtype="f32"):
     dw (N, K) of dw_dtype)."""
     return (grad_input(dy, packed, w_scale),
             grad_weight(dy, xq, a_scale, out_dtype=dw_dtype))
+
+
+# --------------------------------------- root-mean-square norm, global norm of the gradients
+
+def _rmsnorm(x, weight, eps, residual, want_y, scale, return_stats, out=None, sum_out=None):
+    M, K = _rows(x, "x")
+    d = x.device
+    y, xq, a_scale, rstd = out, None, None, None
+    if want_y and y is None:
+        y = torch.empty_like(x)
+    if scale is not None:
+        xq = torch.empty_like(x, dtype=torch.int8)
+        a_scale = x.new_empty(M, dtype=torch.float32)
+    if return_stats:
+        rstd = x.new_empty(M, dtype=torch.float32)
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out goes with a residual")
+    elif sum_out is None:
+        sum_out = torch.empty_like(x)
+    ptr = lambda t: None if t is None else t.data_ptr()  # our own allocations
+    bf = torch.bfloat16
+    _run("bitnet_rmsnorm", d, _arg(x, bf, "x", (M, K), d), _arg(residual, bf, "residual", (M, K), d),
+         _arg(weight, torch.float32, "weight", (K,), d), float(eps), M, K,
+         _arg(sum_out, bf, "sum_out", (M, K), d), _arg(y, bf, "out", (M, K), d), ptr(xq), ptr(a_scale),
+         0 if scale is None else scale, ptr(rstd))
+    return y, xq, a_scale, sum_out, rstd
+
+
+def rmsnorm(x, weight=None, eps=1e-5, residual=None, return_stats=False, out=None, sum_out=None):
+    """Root-mean-square norm of bf16 (M, K) over K with fp32 weight (None: 1) -> bf16 y.  With a
+    residual the norm is of bf16(x + residual), which comes back too (in sum_out, which may be x or
+    residual itself).  Returns y, then the sum with a residual, then the fp32 (M,) rstd that
+    rmsnorm_backward takes with return_stats."""
+    y, _, _, s, rstd = _rmsnorm(x, weight, eps, residual, True, None, return_stats, out, sum_out)
+    more = ((s,) if residual is not None else ()) + ((rstd,) if return_stats else ())
+    return (y,) + more if more else y
+
+
+def rmsnorm_quant(x, weight=None, eps=1e-5, residual=None, scale="absmax", return_y=False,
+                  return_stats=False, sum_out=None):
+    """rmsnorm with the int8 codes of its output in one launch: what quant_act (scale "absmax") or
+    quant_act_pow2 ("pow2") gives for rmsnorm's y.  Returns (xq, a_scale), then the sum with a
+    residual, then y with return_y, then rstd with return_stats."""
+    y, xq, a, s, rstd = _rmsnorm(x, weight, eps, residual, return_y, _scale_code(scale), return_stats,
+                                 None, sum_out)
+    return ((xq, a) + ((s,) if residual is not None else ()) + ((y,) if return_y else ()) +
+            ((rstd,) if return_stats else ()))
+
+
+def rmsnorm_backward(dy, x, weight, rstd, x_scale=None, dresidual=None, need_sums=True,
+                     workspace=None):
+    """(dx bf16 (M, K), dweight fp32 (K,)) of rmsnorm; dweight is None with need_sums=False.  x: what
+    was normalized (the sum, with a residual) in bf16, or its 8-bit checkpoint (int8 codes) with
+    x_scale.  dresidual: the gradient that reaches the sum along the residual stream, added to dx.
+    workspace: uint8 scratch of bitnet_rmsnorm_backward_workspace_size bytes (allocated by
+    default)."""
+    M, K = _rows(dy, "dy")
+    d = dy.device
+    dx = torch.empty_like(dy)
+    dweight = None
+    ws_ptr, ws_bytes, ws = None, 0, None
+    if need_sums:
+        dweight = dy.new_empty(K, dtype=torch.float32)
+        need = int(lib().bitnet_rmsnorm_backward_workspace_size(M, K))
+        ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
+    _run("bitnet_rmsnorm_backward", d, _arg(dy, torch.bfloat16, "dy", (M, K), d),
+         _arg(x, torch.bfloat16 if x_scale is None else torch.int8, "x", (M, K), d),
+         _arg(x_scale, torch.float32, "x_scale", (M,), d),
+         _arg(weight, torch.float32, "weight", (K,), d), _arg(rstd, torch.float32, "rstd", (M,), d),
+         _arg(dresidual, torch.bfloat16, "dresidual", (M, K), d), M, K, dx.data_ptr(),
+         None if dweight is None else dweight.data_ptr(), ws_ptr, ws_bytes)
+    return dx, dweight
+
+
+_GRAD_CODES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+
+
+def _grad_list(tensors, name, device):
+    """Host arrays (pointers, sizes, types) of a list of fp32 and bf16 tensors on one device."""
+    ptrs, sizes, codes = [], [], []
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}[{i}] must be a torch.Tensor")
+        code = _GRAD_CODES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name}[{i}] must be torch.float32 or torch.bfloat16, got {t.dtype}")
+        ptrs.append(_arg(t, t.dtype, f"{name}[{i}]", None, device))
+        sizes.append(t.numel())
+        codes.append(code)
+    n = len(ptrs)
+    return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*codes))
+
+
+def _grad_device(grads):
+    if len(grads) == 0:
+        return torch.device("cuda", torch.cuda.current_device())
+    if not isinstance(grads[0], torch.Tensor):
+        raise TypeError("grads[0] must be a torch.Tensor")
+    if not grads[0].is_cuda:
+        raise ValueError("grads[0] must be a device tensor (the library has no CPU path)")
+    return grads[0].device
+
+
+def grad_norm(grads, out=None, workspace=None):
+    """2-norm of all values of a list of fp32 and bf16 tensors together, as an fp32 scalar tensor (out,
+    if given).  No synchronization.  workspace: uint8 scratch of bitnet_grad_norm_workspace_size
+    bytes (allocated by default)."""
+    grads = list(grads)
+    d = _grad_device(grads)
+    P, N, T = _grad_list(grads, "grads", d)
+    if out is None:
+        out = torch.empty((), dtype=torch.float32, device=d)
+    need = int(lib().bitnet_grad_norm_workspace_size(len(grads))) if workspace is None else 0
+    ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
+    _run("bitnet_grad_norm", d, len(grads), P, N, T, _arg(out, torch.float32, "out", (), d), ws_ptr,
+         ws_bytes)
+    return out
+
+
+def clip_grads(grads, max_norm, norm=None, out=None, workspace=None):
+    """Scale fp32 and bf16 gradients by min(1, max_norm / (norm + 1e-6)), in place or into the list
+    `out`, and return their norm (an fp32 scalar tensor).  norm: the norm to go by (e.g. one reduced
+    over several GPUs) instead of the gradients' own.  No synchronization.  The tensors may not
+    overlap.  workspace: as in grad_norm."""
+    grads = list(grads)
+    d = _grad_device(grads)
+    P, N, T = _grad_list(grads, "grads", d)
+    O = P
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("out must have one tensor per gradient")
+        O = (ctypes.c_void_p * len(out))(*[_arg(o, g.dtype, f"out[{i}]", tuple(g.shape), d)
+                                           for i, (o, g) in enumerate(zip(out, grads))])
+    ws_ptr, ws_bytes, ws = None, 0, None
+    norm_in = _arg(norm, torch.float32, "norm", (), d)
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=d)
+        need = int(lib().bitnet_grad_norm_workspace_size(len(grads))) if workspace is None else 0
+        ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
+    _run("bitnet_clip_grads", d, len(grads), P, O, N, T, float(max_norm), norm_in,
+         norm.data_ptr() if norm_in is None else None, ws_ptr, ws_bytes)
+    return norm
+
+
+# --------------------------------------------------------------------- mixture of experts
+
+MAX_EXPERTS = 1024
+
+
+def expert_order(ids, n_experts, workspace=None):
+    """Stable order of the choices ids (T, J), int32 or int64, by expert: (rows, offsets, slots), all
+    int32.  rows (T * J,): the token of each sorted row; offsets (n_experts + 1,): first row of each
+    expert; slots (T, J): the row of each choice.  Choices outside 0 .. n_experts - 1 (padding)
+    are dropped: slot -1, and the rows behind offsets[-1] have token -1."""
+    T, J = _rows(ids, "ids")
+    d = ids.device
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+    E = int(n_experts)
+    rows = torch.empty((T * J,), dtype=torch.int32, device=d)
+    offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=d)
+    slots = torch.empty((T, J), dtype=torch.int32, device=d)
+    need = int(lib().bitnet_expert_order_workspace_size(T * J, E)) if workspace is None else 0
+    ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
+    _run("bitnet_expert_order", d, _arg(ids, ids.dtype, "ids", (T, J), d),
+         int(ids.dtype is torch.int64), T, J, E, rows.data_ptr(), offsets.data_ptr(),
+         slots.data_ptr(), ws_ptr, ws_bytes)
+    return rows, offsets, slots
+
+
+def _experts_shape(packed, name):
+    """(E, N, K) of one expert weight stack (E, N, K / 4)."""
+    if not isinstance(packed, torch.Tensor) or packed.dim() != 3:
+        raise ValueError(f"{name} must be a (E, N, K / 4) tensor")
+    E, N, K4 = packed.shape
+    return E, N, 4 * K4
+
+
+def _experts_weights(packed, w_scale, d):
+    """(E, K, row counts, host arrays) of up to MAX_GROUPS weight stacks over the same input."""
+    G = len(packed)
+    if G == 0 or len(w_scale) != G:
+        raise ValueError("packed and w_scale must have the same length, at least 1")
+    E, _, K = _experts_shape(packed[0], "packed[0]")
+    Ns = [_experts_shape(t, f"packed[{g}]")[1] for g, t in enumerate(packed)]
+    ptrs, sizes = _ARRAYS[G - 1] if G <= MAX_GROUPS else (ctypes.c_void_p * G, ctypes.c_int64 * G)
+    P = ptrs(*[_arg(t, torch.uint8, "packed", (E, n, K // 4), d) for t, n in zip(packed, Ns)])
+    S = ptrs(*[_arg(t, torch.float32, "w_scale", (E, n), d) for t, n in zip(w_scale, Ns)])
+    return E, K, Ns, ptrs, P, S, sizes(*Ns)
+
+
+def gemm_experts_grouped(xq, a_scale, offsets, packed, w_scale, out_dtype="f32", rows=None, out=None):
+    """Product of every expert's rows with its own ternary weights, for up to MAX_GROUPS weight stacks
+    that read the same activations (gate and up), in one launch: the list of (P, N_g) outputs.
+
+    xq, a_scale: int8 (T, K), fp32 (T,).  offsets: int32 (E + 1,), first row of each expert.  packed /
+    w_scale: sequences of uint8 (E, N_g, K / 4), fp32 (E, N_g).  rows: int32 (P,), the token of each
+    row (expert_order); None: xq is in the rows' order already.  Rows behind offsets[-1] are not
+    written."""
+    T, K = _rows(xq, "xq")
+    d = xq.device
+    E, Kw, Ns, ptrs, W, S, NN = _experts_weights(packed, w_scale, d)
+    if Kw != K:
+        raise ValueError(f"packed has {Kw} columns, xq {K}")
+    P = T if rows is None else rows.numel()
+    code = _out_code(out_dtype)
+    outs = list(out) if out is not None else [None] * len(Ns)
+    if len(outs) != len(Ns):
+        raise ValueError("out must have one tensor per group")
+    outs = [_alloc_out(o, P, n, code, d) for o, n in zip(outs, Ns)]
+    O = ptrs(*[_arg(o, _OUT_TORCH[code], "out", (P, n), d) for o, n in zip(outs, Ns)])
+    _run("bitnet_gemm_experts", d, _arg(xq, torch.int8, "xq", (T, K), d),
+         _arg(a_scale, torch.float32, "a_scale", (T,), d), T, _arg(rows, torch.int32, "rows", (P,), d),
+         _arg(offsets, torch.int32, "offsets", (E + 1,), d), P, E, K, len(Ns), W, S, NN, O, code)
+    return outs
+
+
+def gemm_experts(xq, a_scale, offsets, packed, w_scale, out_dtype="f32", rows=None, out=None):
+    """gemm_experts_grouped for one weight stack: (P, N)."""
+    return gemm_experts_grouped(xq, a_scale, offsets, [packed], [w_scale], out_dtype, rows,
+                                None if out is None else [out])[0]
+
+
+def grad_input_experts_grouped(dy, offsets, packed, w_scale, out=None):
+    """Gradient of gemm_experts_grouped with respect to its activations, bf16 (P, K) in the rows'
+    order (combine_experts(dx, slots) adds up the rows of a token).
+
+    dy: sequence of bf16 (P, N_g).  Rows behind offsets[-1] are not written."""
+    if len(dy) == 0 or len(dy) != len(packed):
+        raise ValueError("dy, packed and w_scale must have the same length, at least 1")
+    P = _rows(dy[0], "dy[0]")[0]
+    d = dy[0].device
+    E, K, Ns, ptrs, W, S, NN = _experts_weights(packed, w_scale, d)
+    if out is None:
+        out = torch.empty((P, K), dtype=torch.bfloat16, device=d)
+    DY = ptrs(*[_arg(t, torch.bfloat16, "dy", (P, n), d) for t, n in zip(dy, Ns)])
+    _run("bitnet_grad_input_experts", d, _arg(offsets, torch.int32, "offsets", (E + 1,), d), P, E, K,
+         len(Ns), DY, W, S, NN, _arg(out, torch.bfloat16, "out", (P, K), d))
+    return out
+
+
+def grad_input_experts(dy, offsets, packed, w_scale, out=None):
+    """grad_input_experts_grouped for one weight stack."""
+    return grad_input_experts_grouped([dy], offsets, [packed], [w_scale], out)
+
+
+def grad_weight_experts(dy, xq, a_scale, offsets, out_dtype="f32", rows=None, out=None,
+                        workspace=None):
+    """Gradient of gemm_experts with respect to the latent weights, (E, N, K): for every expert
+    dy^T (xq / a_scale) over its rows; zeros for an expert without rows.  dy: bf16 (P, N); xq,
+    a_scale, rows: as in gemm_experts_grouped.  workspace: with rows, uint8 scratch of
+    bitnet_grad_weight_experts_workspace_size bytes (allocated by default)."""
+    P, N = _rows(dy, "dy")
+    T, K = _rows(xq, "xq")
+    d = dy.device
+    code = _out_code(out_dtype)
+    if code == OUT_I32:
+        raise ValueError("the weight gradient is fp32 or bf16")
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be a (E + 1,) tensor")
+    E = offsets.numel() - 1
+    if out is None:
+        out = torch.empty((E, N, K), dtype=_OUT_TORCH[code], device=d)
+    need = (int(lib().bitnet_grad_weight_experts_workspace_size(P, K))
+            if workspace is None and rows is not None else 0)
+    ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
+    _run("bitnet_grad_weight_experts", d, _arg(dy, torch.bfloat16, "dy", (P, N), d),
+         _arg(xq, torch.int8, "xq", (T, K), d), _arg(a_scale, torch.float32, "a_scale", (T,), d), T,
+         _arg(rows, torch.int32, "rows", (P,), d), _arg(offsets, torch.int32, "offsets", (E + 1,), d), P,
+         E, N, K, _arg(out, _OUT_TORCH[code], "out", (E, N, K), d), code, ws_ptr, ws_bytes)
+    return out
+
+
+def combine_experts(y, slots, weights=None, out=None):
+    """Weighted sum of a token's rows, bf16 (T, D): sum_j weights[t, j] y[slots[t, j]] from y bf16
+    (P, D), slots int32 (T, J) and weights fp32 (T, J) (None: 1, e.g. for the gradient of a
+    gather).  Slots of -1 add nothing."""
+    P, D = _rows(y, "y")
+    T, J = _rows(slots, "slots")
+    d = y.device
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.bfloat16, device=d)
+    _run("bitnet_combine_experts", d, _arg(y, torch.bfloat16, "y", (P, D), d),
+         _arg(slots, torch.int32, "slots", (T, J), d),
+         _arg(weights, torch.float32, "weights", (T, J), d), T, J, P, D,
+         _arg(out, torch.bfloat16, "out", (T, D), d))
+    return out
+
+
+def combine_experts_backward(dout, y, slots, weights=None, out=None):
+    """(dy bf16 (P, D), dweights fp32 (T, J)) of combine_experts from dout bf16 (T, D); dweights is
+    None without weights.  Rows that no slot names are not written; no two slots may name the same
+    row."""
+    P, D = _rows(y, "y")
+    T, J = _rows(slots, "slots")
+    d = y.device
+    if out is None:
+        out = torch.empty_like(y)
+    dweights = None if weights is None else torch.empty_like(weights)
+    _run("bitnet_combine_experts_backward", d, _arg(dout, torch.bfloat16, "dout", (T, D), d),
+         _arg(y, torch.bfloat16, "y", (P, D), d), _arg(slots, torch.int32, "slots", (T, J), d),
+         _arg(weights, torch.float32, "weights", (T, J), d), T, J, P, D,
+         _arg(out, torch.bfloat16, "out", (P, D), d),
+         None if dweights is None else dweights.data_ptr())
+    return out, dweights

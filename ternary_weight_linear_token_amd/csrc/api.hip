@@ -3,11 +3,13 @@
 // Every entry point validates its arguments on the host, before any HIP call, and
 // returns a bitnet_status code; nothing throws across the ABI.  Work is enqueued on the
 // caller's stream; nothing here synchronizes or allocates.
+#include <algorithm>
 #include <atomic>
 #include <cfloat>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
 
 #include "bitnet_w2a8.h"
 #include "kernels.hpp"
@@ -645,6 +647,295 @@ int bitnet_grad_weight(const uint16_t* dy, const int8_t* xq, const float* a_scal
     if ((st = check_device())) return st;
     return record_hip(bitnet::launch_grad_weight(dy, xq, a_scale, M, N, K, dw, out_dtype, workspace,
                                                  ws_bytes, as_stream(stream)));
+}
+
+// ---- root-mean-square norm, global norm of the gradients ----
+
+int bitnet_rmsnorm(const uint16_t* x, const uint16_t* residual, const float* weight, float eps,
+                   int64_t M, int64_t K, uint16_t* sum, uint16_t* y, int8_t* xq, float* a_scale,
+                   int scale, float* rstd, void* stream) {
+    if (!valid_scale(scale)) return BITNET_ERR_INVALID_ARG;
+    if (!(eps >= FLT_MIN) || eps > FLT_MAX) return BITNET_ERR_INVALID_ARG;
+    int st = check_shape(M, 0, K);
+    if (st) return st;
+    if (M == 0) return BITNET_OK;
+    if (!x || (!y && !xq) || (xq != nullptr) != (a_scale != nullptr) ||
+        (residual != nullptr) != (sum != nullptr))
+        return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum) || !aligned16(y) ||
+        !aligned16(xq) || !aligned16(a_scale) || !aligned16(rstd))
+        return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_rmsnorm(x, residual, weight, eps, M, K, sum, y, xq, a_scale,
+                                             scale == BITNET_SCALE_POW2, rstd, as_stream(stream)));
+}
+
+size_t bitnet_rmsnorm_backward_workspace_size(int64_t M, int64_t K) {
+    if (check_shape(M, 0, K) != BITNET_OK || M == 0) return 0;
+    return bitnet::rmsnorm_back_workspace_size(M, K);
+}
+
+int bitnet_rmsnorm_backward(const uint16_t* dy, const void* x, const float* x_scale,
+                            const float* weight, const float* rstd, const uint16_t* dresidual,
+                            int64_t M, int64_t K, uint16_t* dx, float* dweight, void* workspace,
+                            size_t ws_bytes, void* stream) {
+    int st = check_shape(M, 0, K);
+    if (st) return st;
+    if (M == 0 && !dweight) return BITNET_OK;
+    if (M > 0 && (!dy || !x || !rstd || !dx)) return BITNET_ERR_INVALID_ARG;
+    if (ws_bytes > 0 && !workspace) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(x_scale) || !aligned16(weight) ||
+        !aligned16(rstd) || !aligned16(dresidual) || !aligned16(dx) || !aligned16(dweight) ||
+        !aligned16(workspace))
+        return BITNET_ERR_UNALIGNED;
+    if (M > 0 && dweight && ws_bytes < bitnet::rmsnorm_back_workspace_size(M, K))
+        return BITNET_ERR_WORKSPACE;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_rmsnorm_back(dy, x, x_scale, weight, rstd, dresidual, M, K, dx,
+                                                  dweight, workspace, as_stream(stream)));
+}
+
+// The lists of the norm and of clipping: pointers aligned to their values, sizes that 63 bits hold
+// in bytes.
+static int check_grads(int64_t count, const void* const* grads, const int64_t* n, const int32_t* dtype) {
+    if (count < 0 || count > INT32_MAX) return BITNET_ERR_INVALID_ARG;
+    if (count > 0 && (!grads || !n || !dtype)) return BITNET_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < count; ++i) {
+        if (dtype[i] != BITNET_OUT_F32 && dtype[i] != BITNET_OUT_BF16) return BITNET_ERR_INVALID_ARG;
+        if (n[i] < 0 || n[i] > INT64_MAX / 8) return BITNET_ERR_INVALID_ARG;
+        if (n[i] == 0) continue;
+        if (!grads[i]) return BITNET_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(grads[i]) & (dtype[i] == BITNET_OUT_F32 ? 3u : 1u))
+            return BITNET_ERR_UNALIGNED;
+    }
+    return BITNET_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+size_t bitnet_grad_norm_workspace_size(int64_t count) {
+    if (count < 0 || count > INT32_MAX) return 0;
+    return bitnet::grad_norm_workspace_size(count > 0 ? count : 1);
+}
+
+int bitnet_grad_norm(int64_t count, const void* const* grads, const int64_t* n, const int32_t* dtype,
+                     float* norm, void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_grads(count, grads, n, dtype);
+    if (st) return st;
+    if (!norm || (ws_bytes > 0 && !workspace)) return BITNET_ERR_INVALID_ARG;
+    if (!aligned4(norm) || !aligned16(workspace)) return BITNET_ERR_UNALIGNED;
+    if (ws_bytes < bitnet_grad_norm_workspace_size(count)) return BITNET_ERR_WORKSPACE;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_grad_norm(count, grads, nullptr, n, dtype, false, 0.0f, nullptr,
+                                               norm, workspace, as_stream(stream)));
+}
+
+// Whether an output overlaps another output, or an input that is not its own (out[i] == grads[i]
+// exactly).  Spans sorted by their start: an output may not begin before the furthest end of the
+// spans in front of it, nor an input before that of the outputs.
+static int check_clip_outputs(int64_t count, const void* const* grads, void* const* out, const int64_t* n,
+                              const int32_t* dtype) {
+    struct Span {
+        uintptr_t begin, end;
+        bool out;
+    };
+    Span* const spans = new (std::nothrow) Span[2 * (size_t)count + 1];
+    if (!spans) {
+        std::snprintf(g_last_hip_error, sizeof g_last_hip_error, "out of host memory");
+        return BITNET_ERR_HIP;
+    }
+    size_t m = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (n[i] == 0) continue;
+        const uintptr_t bytes = (uintptr_t)n[i] * (dtype[i] == BITNET_OUT_F32 ? 4 : 2);
+        const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(out[i]);
+        spans[m++] = {o, o + bytes, true};
+        if (g != o) spans[m++] = {g, g + bytes, false};
+    }
+    std::sort(spans, spans + m, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    uintptr_t any = 0, outs = 0;
+    int st = BITNET_OK;
+    for (size_t i = 0; i < m && st == BITNET_OK; ++i) {
+        if (spans[i].begin < (spans[i].out ? any : outs)) st = BITNET_ERR_INVALID_ARG;
+        any = std::max(any, spans[i].end);
+        if (spans[i].out) outs = std::max(outs, spans[i].end);
+    }
+    delete[] spans;
+    return st;
+}
+
+int bitnet_clip_grads(int64_t count, const void* const* grads, void* const* out, const int64_t* n,
+                      const int32_t* dtype, float max_norm, const float* norm_in, float* norm_out,
+                      void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_grads(count, grads, n, dtype);
+    if (st) return st;
+    if (!(max_norm >= 0.0f) || max_norm > FLT_MAX) return BITNET_ERR_INVALID_ARG;
+    if (count > 0 && !out) return BITNET_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < count; ++i) {
+        if (n[i] == 0) continue;
+        if (!out[i]) return BITNET_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(out[i]) & (dtype[i] == BITNET_OUT_F32 ? 3u : 1u))
+            return BITNET_ERR_UNALIGNED;
+    }
+    if (ws_bytes > 0 && !workspace) return BITNET_ERR_INVALID_ARG;
+    if (!aligned4(norm_in) || !aligned4(norm_out) || !aligned16(workspace)) return BITNET_ERR_UNALIGNED;
+    if (!norm_in && ws_bytes < bitnet_grad_norm_workspace_size(count)) return BITNET_ERR_WORKSPACE;
+    if ((st = check_clip_outputs(count, grads, out, n, dtype))) return st;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_grad_norm(count, grads, out, n, dtype, true, max_norm, norm_in,
+                                               norm_out, workspace, as_stream(stream)));
+}
+
+// ---- mixture of experts ----
+
+static int check_experts(int64_t P, int64_t E, int64_t K, int64_t groups, const int64_t* N) {
+    if (E < 1 || E > BITNET_MAX_EXPERTS) return BITNET_ERR_INVALID_ARG;
+    return check_grad_groups(P, K, groups, N);  // P within BITNET_GRAD_MAX_M, N within BITNET_MAX_K
+}
+
+// Tokens behind the rows: as many as rows without a gather, else within 31 bits of codes.
+static bool valid_tokens(int64_t T, const int32_t* rows, int64_t P, int64_t K) {
+    if (T < 0 || T > INT32_MAX) return false;
+    return rows ? T * K <= INT32_MAX : T == P;
+}
+
+size_t bitnet_expert_order_workspace_size(int64_t P, int64_t E) {
+    if (P < 0 || P > BITNET_GRAD_MAX_M || E < 1 || E > BITNET_MAX_EXPERTS) return 0;
+    return bitnet::expert_order_workspace_size(P, E);
+}
+
+int bitnet_expert_order(const void* ids, int wide, int64_t T, int64_t J, int64_t E, int32_t* rows,
+                        int32_t* offsets, int32_t* slots, void* workspace, size_t ws_bytes,
+                        void* stream) {
+    if (T < 0 || T > BITNET_GRAD_MAX_M || J < 1 || J > BITNET_MAX_EXPERTS || T * J > BITNET_GRAD_MAX_M ||
+        E < 1 || E > BITNET_MAX_EXPERTS || (wide != 0 && wide != 1))
+        return BITNET_ERR_INVALID_ARG;
+    if (!offsets || (T > 0 && (!ids || !rows || !slots)) || (ws_bytes > 0 && !workspace))
+        return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(ids) || !aligned16(rows) || !aligned16(offsets) || !aligned16(slots) ||
+        !aligned16(workspace))
+        return BITNET_ERR_UNALIGNED;
+    if (ws_bytes < bitnet::expert_order_workspace_size(T * J, E)) return BITNET_ERR_WORKSPACE;
+    const int st = check_device();
+    if (st) return st;
+    return record_hip(bitnet::launch_expert_order(ids, wide, T, J, E, rows, offsets, slots, workspace,
+                                                  as_stream(stream)));
+}
+
+int bitnet_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T, const int32_t* rows,
+                        const int32_t* offsets, int64_t P, int64_t E, int64_t K, int64_t groups,
+                        const uint8_t* const* packed, const float* const* w_scale, const int64_t* N,
+                        void* const* out, int out_dtype, void* stream) {
+    if (!valid_dtype(out_dtype)) return BITNET_ERR_INVALID_ARG;
+    int st = check_experts(P, E, K, groups, N);
+    if (st) return st;
+    if (!valid_tokens(T, rows, P, K)) return BITNET_ERR_INVALID_ARG;
+    if (!packed || !w_scale || !out) return BITNET_ERR_INVALID_ARG;
+    int64_t total_n = 0;
+    for (int64_t g = 0; g < groups; ++g) total_n += N[g];
+    if (P == 0 || total_n == 0) return BITNET_OK;
+    if (!offsets || (T > 0 && (!xq || !a_scale))) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(xq) || !aligned16(a_scale) || !aligned16(rows) || !aligned16(offsets))
+        return BITNET_ERR_UNALIGNED;
+    for (int64_t g = 0; g < groups; ++g) {
+        if (N[g] == 0) continue;
+        if (!packed[g] || !w_scale[g] || !out[g]) return BITNET_ERR_INVALID_ARG;
+        if (!aligned16(packed[g]) || !aligned16(w_scale[g]) || !aligned16(out[g]))
+            return BITNET_ERR_UNALIGNED;
+    }
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_gemm_experts(xq, a_scale, T, rows, offsets, P, E, K, (int)groups,
+                                                  packed, w_scale, N, out, out_dtype, as_stream(stream)));
+}
+
+int bitnet_grad_input_experts(const int32_t* offsets, int64_t P, int64_t E, int64_t K, int64_t groups,
+                              const uint16_t* const* dy, const uint8_t* const* packed,
+                              const float* const* w_scale, const int64_t* N, uint16_t* dx,
+                              void* stream) {
+    int st = check_experts(P, E, K, groups, N);
+    if (st) return st;
+    if (!dy || !packed || !w_scale) return BITNET_ERR_INVALID_ARG;
+    if (P == 0) return BITNET_OK;
+    if (!offsets || !dx) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(offsets) || !aligned16(dx)) return BITNET_ERR_UNALIGNED;
+    for (int64_t g = 0; g < groups; ++g) {
+        if (N[g] == 0) continue;
+        if (!dy[g] || !packed[g] || !w_scale[g]) return BITNET_ERR_INVALID_ARG;
+        if (!aligned16(dy[g]) || !aligned16(packed[g]) || !aligned16(w_scale[g]))
+            return BITNET_ERR_UNALIGNED;
+    }
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_grad_input_experts(dy, offsets, P, E, packed, w_scale, N,
+                                                        (int)groups, K, dx, as_stream(stream)));
+}
+
+// Codes in the rows' order, then their scales.
+static size_t gathered_codes(int64_t P, int64_t K) { return ((size_t)(P * K) + 15) / 16 * 16; }
+
+size_t bitnet_grad_weight_experts_workspace_size(int64_t P, int64_t K) {
+    if (check_shape(P, 0, K) != BITNET_OK || P > BITNET_GRAD_MAX_M || P == 0) return 0;
+    return gathered_codes(P, K) + (size_t)P * 4;
+}
+
+int bitnet_grad_weight_experts(const uint16_t* dy, const int8_t* xq, const float* a_scale, int64_t T,
+                               const int32_t* rows, const int32_t* offsets, int64_t P, int64_t E,
+                               int64_t N, int64_t K, void* dw, int out_dtype, void* workspace,
+                               size_t ws_bytes, void* stream) {
+    if (out_dtype != BITNET_OUT_F32 && out_dtype != BITNET_OUT_BF16) return BITNET_ERR_INVALID_ARG;
+    int st = check_experts(P, E, K, 1, &N);
+    if (st) return st;
+    if (!valid_tokens(T, rows, P, K)) return BITNET_ERR_INVALID_ARG;
+    if (N == 0) return BITNET_OK;
+    if (!dw || !offsets || (ws_bytes > 0 && !workspace)) return BITNET_ERR_INVALID_ARG;
+    if (P > 0 && (!dy || (T > 0 && (!xq || !a_scale)))) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(xq) || !aligned16(a_scale) || !aligned16(rows) ||
+        !aligned16(offsets) || !aligned16(dw) || !aligned16(workspace))
+        return BITNET_ERR_UNALIGNED;
+    if (rows && ws_bytes < bitnet_grad_weight_experts_workspace_size(P, K)) return BITNET_ERR_WORKSPACE;
+    if ((st = check_device())) return st;
+    if (rows && P > 0) {
+        int8_t* const xs = static_cast<int8_t*>(workspace);
+        float* const as = reinterpret_cast<float*>(xs + gathered_codes(P, K));
+        st = record_hip(bitnet::launch_gather_codes(xq, a_scale, T, rows, P, K, xs, as, as_stream(stream)));
+        if (st) return st;
+        xq = xs;
+        a_scale = as;
+    }
+    return record_hip(bitnet::launch_grad_weight_experts(dy, xq, a_scale, offsets, P, E, N, K, dw,
+                                                         out_dtype, as_stream(stream)));
+}
+
+static int check_combine(int64_t T, int64_t J, int64_t P, int64_t D) {
+    if (J < 1 || J > BITNET_MAX_EXPERTS || P < 0 || P > BITNET_GRAD_MAX_M || T > BITNET_GRAD_MAX_M)
+        return BITNET_ERR_INVALID_ARG;
+    return check_shape(T, 0, D);
+}
+
+int bitnet_combine_experts(const uint16_t* y, const int32_t* slots, const float* weights, int64_t T,
+                           int64_t J, int64_t P, int64_t D, uint16_t* out, void* stream) {
+    int st = check_combine(T, J, P, D);
+    if (st) return st;
+    if (T == 0) return BITNET_OK;
+    if (!slots || !out || (P > 0 && !y)) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(y) || !aligned16(slots) || !aligned16(weights) || !aligned16(out))
+        return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_combine(y, slots, weights, T, J, P, D, out, as_stream(stream)));
+}
+
+int bitnet_combine_experts_backward(const uint16_t* dout, const uint16_t* y, const int32_t* slots,
+                                    const float* weights, int64_t T, int64_t J, int64_t P, int64_t D,
+                                    uint16_t* dy, float* dweights, void* stream) {
+    int st = check_combine(T, J, P, D);
+    if (st) return st;
+    if (T == 0) return BITNET_OK;
+    if (!dout || !slots || (P > 0 && (!dy || (dweights && !y)))) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(dout) || !aligned16(y) || !aligned16(slots) || !aligned16(weights) ||
+        !aligned16(dy) || !aligned16(dweights))
+        return BITNET_ERR_UNALIGNED;
+    if ((st = check_device())) return st;
+    return record_hip(bitnet::launch_combine_back(dout, y, slots, weights, T, J, P, D, dy, dweights,
+                                                  as_stream(stream)));
 }
 
 }  // extern "C"

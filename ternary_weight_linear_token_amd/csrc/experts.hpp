@@ -1,0 +1,78 @@
+// experts.hpp -- how the blocks of a product grouped by expert find their rows: shared by the
+// forward product (experts.hip) and the gradients (grad.hip).
+//
+// The rows of a call are sorted by expert and offsets[e] .. offsets[e + 1] are those of expert e; the
+// offsets lie in device memory, so the host knows neither the counts nor the number of tiles.
+// It launches as many blocks as any counts could need (min(E, P) experts may each end in a
+// partial tile), and every wave of a block counts the tiles itself: lane l takes the experts
+// per * l .., a scan over the wave gives the tiles before each, and a ballot the expert of a tile.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace bitnet {
+
+// Most tiles of `bm` rows that P rows of E experts can make.
+inline int64_t expert_tiles(int64_t P, int64_t E, int bm) {
+    const int64_t e = E < P ? E : P;
+    return (P + e * (bm - 1)) / bm;
+}
+
+// Inclusive sum over the wave (every lane active).
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31
+    return v;
+}
+
+// Rows of expert e, whatever the offsets hold: inside 0 .. P, none where they run backwards.
+struct ExpertRows {
+    int first, count;
+};
+__device__ __forceinline__ ExpertRows expert_rows(const int* offsets, int e, int P) {
+    const int a = min(max(offsets[e], 0), P), b = min(max(offsets[e + 1], 0), P);
+    return {a, b > a ? b - a : 0};
+}
+
+// The tiles of BM rows of all experts, in the experts' order.
+template <int BM>
+struct ExpertTiles {
+    const int* offsets;
+    int E, P, per, sum, scan;
+    int total;  // uniform
+
+    __device__ __forceinline__ ExpertTiles(const int* off, int experts, int rows)
+        : offsets(off), E(experts), P(rows), per((experts + 63) >> 6), sum(0) {
+        const int lane = threadIdx.x & 63;
+        for (int i = 0; i < per; ++i) {
+            const int e = lane * per + i;
+            if (e < E) sum += (expert_rows(offsets, e, P).count + BM - 1) / BM;
+        }
+        scan = wave_scan(sum);
+        total = __builtin_amdgcn_readlane(scan, 63);
+    }
+
+    // Expert, first row and number of rows (at most BM) of tile t < total; all uniform.
+    __device__ __forceinline__ void find(int t, int& e, int& first, int& rows) const {
+        const uint64_t past = __ballot(scan > t);
+        const int l = (int)__builtin_ctzll(past);
+        int left = t - (__builtin_amdgcn_readlane(scan, l) - __builtin_amdgcn_readlane(sum, l));
+        e = l * per;
+        for (;; ++e) {
+            const ExpertRows r = expert_rows(offsets, e, P);
+            const int n = (r.count + BM - 1) / BM;
+            if (left < n || e == E - 1) {
+                first = r.first + left * BM;
+                rows = min(BM, r.count - left * BM);
+                return;
+            }
+            left -= n;
+        }
+    }
+};
+
+}  // namespace bitnet

@@ -57,6 +57,7 @@
 #include <utility>
 
 #include "device_common.hpp"
+#include "experts.hpp"
 #include "kernels.hpp"
 
 namespace bitnet {
@@ -93,6 +94,14 @@ struct GradArgs {
     int out_dtype;
     void* out;    // (I, J)
     float* part;  // (slices, I, J) when slices > 1
+    // grouped by expert (EXPERTS): the P rows of dy are sorted, those of expert e are offsets[e] ..;
+    // b, scale (MODE 1) and out (MODE 0) hold one matrix per expert.  MODE 1: I is P; MODE 0: L[0].
+    const int* offsets;
+    int E, P;
+};
+
+struct NoTiles {
+    __device__ __forceinline__ NoTiles(const int*, int, int) {}
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int bytes) {
@@ -134,7 +143,7 @@ __device__ __forceinline__ int chunk(int i, int c) {
     return i * (2 * BL) + ((c ^ (CPR == 8 ? (i & 7) : ((i >> 1) & 3))) << 4);
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, int D, int W, Rows ROWS>
+template <int MODE, int BM, int BN, int WM, int WN, int G, int BL, int D, int W, Rows ROWS, bool EXPERTS>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel(GradArgs p) {
     constexpr int WPG = (BM / WM) * (BN / WN);  // waves of a group
     constexpr int TG = 64 * WPG;                // threads of a group
@@ -164,27 +173,46 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     uint8_t* const stage = lds + 2 * g * kBuf;
 
     // tile of this block: consecutive blocks go to different XCDs, so each XCD gets a
-    // contiguous run of tiles; runs walk panels of kPanel tile rows
-    const int tiles = p.tiles_i * p.tiles_j, total = tiles * p.slices;
+    // contiguous run of tiles; runs walk panels of kPanel tile rows.  Grouped by expert, MODE 0
+    // has the tiles of every expert behind one another, MODE 1 the row tiles of all experts.
+    int tiles_i = p.tiles_i;
+    std::conditional_t<EXPERTS && MODE == 1, ExpertTiles<BM>, NoTiles> rows_of(p.offsets, p.E, p.P);
+    if constexpr (EXPERTS && MODE == 1) tiles_i = rows_of.total;
+    const int tiles = tiles_i * p.tiles_j, total = tiles * (EXPERTS ? (MODE == 0 ? p.E : 1) : p.slices);
     int t = blockIdx.x;
     {
         const int xcd = t & 7, q = total >> 3, r = total & 7;
+        if (EXPERTS && (t >> 3) >= q + (xcd < r ? 1 : 0)) return;  // fewer tiles than there might be
         t = xcd * q + (xcd < r ? xcd : r) + (t >> 3);
     }
-    const int slice = t / tiles;
+    const int slice = t / tiles;  // EXPERTS, MODE 0: the expert
     t -= slice * tiles;
     constexpr int kPanel = 4;
     const int panel = t / (kPanel * p.tiles_j);
-    const int ph = p.tiles_i - panel * kPanel < kPanel ? p.tiles_i - panel * kPanel : kPanel;
+    const int ph = tiles_i - panel * kPanel < kPanel ? tiles_i - panel * kPanel : kPanel;
     const int tp = t - panel * kPanel * p.tiles_j;
     const int ti = panel * kPanel + tp % ph, tj = tp / ph;
-    const int i0 = ti * BM, j0 = tj * BN;
-    const int I = p.I, J = p.J;
+    const int j0 = tj * BN, J = p.J;
+    int i0 = ti * BM, I = p.I, expert = 0, row0 = 0, L = p.L[0], first_step = 0, steps = 0;
+    if constexpr (!EXPERTS) {
+        first_step = (int)((int64_t)p.steps * slice / p.slices);
+        steps = (int)((int64_t)p.steps * (slice + 1) / p.slices) - first_step;
+    } else if constexpr (MODE == 0) {
+        expert = slice;
+        const ExpertRows r = expert_rows(p.offsets, expert, p.P);
+        row0 = r.first;
+        L = r.count;
+        steps = (L + BL - 1) / BL;
+    } else {
+        int rows;
+        rows_of.find(ti, expert, i0, rows);
+        I = i0 + rows;
+        steps = p.steps;
+    }
 
     // steps of this block: [s0, s1), group g takes s0 + g, s0 + g + G, ...; every group runs
     // nsteps steps and multiplies zeros past its last one
-    const int s0 = (int)((int64_t)p.steps * slice / p.slices);
-    const int s1 = (int)((int64_t)p.steps * (slice + 1) / p.slices);
+    const int s0 = first_step, s1 = first_step + steps;
     const int nsteps = (s1 - s0 + G - 1) / G;
 
     // ---- loads: the step to load next ----
@@ -192,7 +220,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     // the step's start to the end of what the block sums of them; at or below zero past the
     // end, where the descriptors are empty and read as zeros.
     int left, end;  // MODE 1: end of the block's share, from the start of group q (padded)
-    int l0 = (s0 + g) * BL, q = 0, L = p.L[0];
+    int l0 = (s0 + g) * BL, q = 0;
     const int row_bytes = J / 4;
     const int rows_a = I - i0 < BM ? I - i0 : BM;  // MODE 1
     const int step_l = G * BL;
@@ -202,15 +230,28 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     // The last element of rows at odd places may lie in the lower half of a dword.  The
     // descriptor covers that dword for the tiles that hold the last column; in MODE 0 it ends
     // before it for the others, of which the first has the column behind the last element.
-    const int up = MODE == 1 || i0 + BM >= I ? 3 : 0;
+    // Grouped by expert, rows may also begin off a dword (skew), and MODE 0 masks rows past the end
+    // by number (kOddEnd).
+    const int up = EXPERTS || MODE == 1 || i0 + BM >= I ? 3 : 0;
     auto whole = [&](int bytes) { return ALIGNED ? bytes : (bytes + up) & ~3; };
+    constexpr bool SKEW = EXPERTS && !ALIGNED;
+    int skew_a = 0, skew_b = 0;
     auto enter = [&]() {  // at l0 of group q
         const int stop = L < end ? L : end;
         left = stop - l0;
         pa = reinterpret_cast<const uint8_t*>(
-            p.dy[q] + (MODE == 0 ? (int64_t)l0 * I + i0 : (int64_t)i0 * L));
-        pb = p.b[q] + (MODE == 0 ? (int64_t)l0 * J + j0 : (int64_t)l0 * row_bytes + j0 / 4);
-        ps = reinterpret_cast<const uint8_t*>(p.scale[q] + l0);
+            p.dy[q] + (MODE == 0 ? (int64_t)(row0 + l0) * I + i0 : (int64_t)i0 * L));
+        pb = p.b[q] + (MODE == 0 ? (int64_t)(row0 + l0) * J + j0
+                                 : ((int64_t)expert * L + l0) * row_bytes + j0 / 4);
+        ps = reinterpret_cast<const uint8_t*>(p.scale[q] + (MODE == 0 ? (int64_t)row0 : (int64_t)expert * L) + l0);
+        if (SKEW) {
+            skew_a = (int)((uintptr_t)pa & 2);
+            pa -= skew_a;
+            if (MODE == 1) {
+                skew_b = (int)((uintptr_t)pb & 3);
+                pb -= skew_b;
+            }
+        }
 #pragma unroll
         for (int n = 0; n < NA; ++n) {
             const int id = tg + n * TG;
@@ -220,7 +261,14 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
                 voff_a[n] = kAFull || id < kAUnits
                                 ? (uint32_t)(id / (BL / 8) * L + 8 * (id % (BL / 8))) * 2
                                 : 0x80000000u;
+            if (SKEW && voff_a[n] != 0x80000000u) voff_a[n] += skew_a;
         }
+        if (SKEW && MODE == 1)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const int id = tg + n * TG;
+                voff_b[n] = (uint32_t)(id / (BN / 16) * row_bytes + 4 * (id % (BN / 16))) + skew_b;
+            }
     };
     end = s1 * BL;
     if constexpr (MODE == 1) {
@@ -230,23 +278,23 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
             L = p.L[++q];
         }
     }
-    enter();
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         const int id = tg + n * TG, l = id / (BN / 16), c = id % (BN / 16);
         voff_b[n] = MODE == 0 ? (uint32_t)(l * J + 16 * c) : (uint32_t)(l * row_bytes + 4 * c);
     }
+    enter();
     __amdgpu_buffer_rsrc_t ra, rb, rs;
     auto describe = [&]() {
         // sizes of at most 256 rows of 2^20 elements: 32 bits hold them
         const bool live = left > 0;
         const int rows = left < BL ? left : BL;
         if constexpr (MODE == 0) {
-            ra = rsrc(pa, live ? whole((rows * I - i0) * 2) : 0);
+            ra = rsrc(pa, live ? whole((rows * I - i0) * 2 + skew_a) : 0);
             rb = rsrc(pb, live ? rows * J - j0 : 0);
         } else {
-            ra = rsrc(pa, live ? whole(rows_a * L * 2) : 0);
-            rb = rsrc(pb, live ? whole(rows * row_bytes - j0 / 4) : 0);
+            ra = rsrc(pa, live ? whole(rows_a * L * 2 + skew_a) : 0);
+            rb = rsrc(pb, live ? whole(rows * row_bytes - j0 / 4 + skew_b) : 0);
         }
         rs = rsrc(ps, live ? rows * 4 : 0);
     };
@@ -559,7 +607,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     // main loop.)
     int pitch = J, tid_out = lane;
     asm volatile("" : "+s"(pitch), "+v"(tid_out));
-    const int64_t base = (int64_t)(i0 + wi * WM) * pitch + j0 + wj * WN;
+    const int64_t base = ((EXPERTS && MODE == 0 ? (int64_t)expert * I : 0) + i0 + wi * WM) * pitch + j0 + wj * WN;
     const int rows = I - i0 - wi * WM, cols = J - j0 - wj * WN;
     const bool inside = rows >= WM && cols >= WN;
     auto emit = [&](auto all, auto put) {
@@ -593,7 +641,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
         else
             emit(std::false_type(), put);
     };
-    if (p.slices > 1) {
+    if (!EXPERTS && p.slices > 1) {
         float* const out = p.part + (int64_t)slice * I * J + base;
         output([&](uint32_t o, float v0, float v1) {
             if constexpr (MODE == 0)
@@ -672,8 +720,9 @@ constexpr GradCfg kCfg[] = {
 constexpr int kCfgs = sizeof(kCfg) / sizeof(kCfg[0]);
 constexpr int kCUs = 256;
 
-// The configuration and number of slices with the least estimated time.
-GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
+// The configuration and number of slices with the least estimated time, of `copies` such products
+// (experts, each unsplit) in one launch.
+GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups, int64_t copies = 0) {
     GradPlan best = {0, 1, 0};
     double best_t = 1e300;
     for (int c = 0; c < kCfgs; ++c) {
@@ -681,8 +730,8 @@ GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
         if (k.mode != mode) continue;
         int64_t steps = 0;
         for (int q = 0; q < groups; ++q) steps += (L[q] + k.bl - 1) / k.bl;
-        const int64_t tiles = ((I + k.bm - 1) / k.bm) * ((J + k.bn - 1) / k.bn);
-        for (int64_t s = 1; s <= 16; ++s) {
+        const int64_t tiles = ((I + k.bm - 1) / k.bm) * ((J + k.bn - 1) / k.bn) * (copies > 0 ? copies : 1);
+        for (int64_t s = 1; s <= (copies > 0 ? 1 : 16); ++s) {
             // at least two steps per group of a slice, at most 64 MB of partial sums
             if (s > 1 && (steps < 2 * s * k.g || s * I * J * 4 > ((int64_t)64 << 20))) break;
             const double per = (double)(((steps + s - 1) / s + k.g - 1) / k.g);
@@ -704,13 +753,13 @@ GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
     return best;
 }
 
-template <int C, Rows ROWS>
+template <int C, Rows ROWS, bool EXPERTS = false>
 void launch_rows(const GradArgs& a, hipStream_t stream) {
     constexpr GradCfg k = kCfg[C];
-    const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices));
+    const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices + (EXPERTS ? 7 : 0)));
     const dim3 block(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g);
-    hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, ROWS>), grid, block, 0,
-                       stream, a);
+    hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, ROWS, EXPERTS>), grid,
+                       block, 0, stream, a);
 }
 
 template <int C>
@@ -721,6 +770,36 @@ void launch_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
         launch_rows<C, kCfg[C].mode == 0 ? kOddEnd : kOdd>(a, stream);
     else
         launch_rows<C, kOdd>(a, stream);
+}
+
+template <int C>
+void launch_experts_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
+    if (aligned)
+        launch_rows<C, kWhole, true>(a, stream);
+    else
+        launch_rows<C, kCfg[C].mode == 0 ? kOddEnd : kOdd, true>(a, stream);
+}
+
+template <size_t... C>
+void launch_experts_any(int cfg, const GradArgs& a, bool aligned, hipStream_t stream, std::index_sequence<C...>) {
+    ((cfg == (int)C ? launch_experts_cfg<(int)C>(a, aligned, stream) : (void)0), ...);
+}
+
+// I and L of a are all rows (MODE 1: I, MODE 0: L[0]); the plan is that of rows spread evenly.
+hipError_t launch_grad_experts(int mode, GradArgs a, const int64_t* L, bool aligned, hipStream_t stream) {
+    const int64_t active = a.E < a.P ? a.E : a.P;
+    const int64_t even = active > 0 ? (a.P + active - 1) / active : 0;
+    const GradPlan pl = mode == 0 ? plan(0, a.I, a.J, &even, 1, a.E) : plan(1, even, a.J, L, a.groups, active);
+    const GradCfg& k = kCfg[pl.cfg];
+    const int64_t ti = mode == 0 ? (a.I + k.bm - 1) / k.bm : expert_tiles(a.P, a.E, k.bm);
+    const int64_t tj = (a.J + k.bn - 1) / k.bn, blocks = ti * tj * (mode == 0 ? a.E : 1);
+    if (blocks + 7 > max_blocks(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g)) return hipErrorInvalidValue;
+    a.tiles_i = (int)ti;
+    a.tiles_j = (int)tj;
+    a.steps = pl.steps;
+    a.slices = mode == 0 ? a.E : 1;
+    launch_experts_any(pl.cfg, a, aligned, stream, std::make_index_sequence<kCfgs>());
+    return hipGetLastError();
 }
 
 template <size_t... C>
@@ -809,6 +888,50 @@ hipError_t launch_grad_weight(const uint16_t* dy, const int8_t* xq, const float*
     a.out = dw;
     a.out_dtype = out_dtype;
     return launch_grad(0, a, &M, N % 2 == 0, workspace, ws_bytes, stream);
+}
+
+hipError_t launch_grad_input_experts(const uint16_t* const* dy, const int* offsets, int64_t P, int64_t E,
+                                     const uint8_t* const* packed, const float* const* w_scale,
+                                     const int64_t* N, int groups, int64_t K, uint16_t* dx, hipStream_t stream) {
+    GradArgs a = {};
+    int64_t L[BITNET_MAX_GROUPS] = {};
+    bool aligned = K % 16 == 0;
+    for (int q = 0; q < groups; ++q) {
+        if (N[q] == 0) continue;  // adds nothing
+        a.dy[a.groups] = dy[q];
+        a.b[a.groups] = packed[q];
+        a.scale[a.groups] = w_scale[q];
+        a.L[a.groups] = (int)N[q];
+        L[a.groups++] = N[q];
+        aligned = aligned && N[q] % 8 == 0;
+    }
+    a.I = (int)P;
+    a.J = (int)K;
+    a.out = dx;
+    a.out_dtype = BITNET_OUT_BF16;
+    a.offsets = offsets;
+    a.E = (int)E;
+    a.P = (int)P;
+    return launch_grad_experts(1, a, L, aligned, stream);
+}
+
+hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, const float* a_scale,
+                                      const int* offsets, int64_t P, int64_t E, int64_t N, int64_t K,
+                                      void* dw, int out_dtype, hipStream_t stream) {
+    GradArgs a = {};
+    a.dy[0] = dy;
+    a.b[0] = reinterpret_cast<const uint8_t*>(xq);
+    a.scale[0] = a_scale;
+    a.L[0] = (int)P;
+    a.groups = 1;
+    a.I = (int)N;
+    a.J = (int)K;
+    a.out = dw;
+    a.out_dtype = out_dtype;
+    a.offsets = offsets;
+    a.E = (int)E;
+    a.P = (int)P;
+    return launch_grad_experts(0, a, nullptr, N % 2 == 0, stream);
 }
 
 }  // namespace bitnet

@@ -141,4 +141,51 @@ hipError_t launch_grad_weight(const uint16_t* dy, const int8_t* xq, const float*
                               int64_t N, int64_t K, void* dw, int out_dtype, void* workspace,
                               size_t ws_bytes, hipStream_t stream);
 
+// Root-mean-square norm of (M, K) rows, of x + res where res is given (its sum is then written to
+// `sum`, which may be x or res); y, codes and rstd are each optional.
+hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* res, const float* w, float eps, int64_t M,
+                          int64_t K, uint16_t* sum, uint16_t* y, int8_t* xq, float* a_scale, int pow2,
+                          float* rstd, hipStream_t stream);
+// Its backward, with dres (optional) added to dx; dweight optional, with it the workspace of
+// rmsnorm_back_workspace_size bytes is needed.  M == 0 only clears dweight.
+size_t rmsnorm_back_workspace_size(int64_t M, int64_t K);
+hipError_t launch_rmsnorm_back(const uint16_t* dy, const void* x, const float* x_scale, const float* w,
+                               const float* rstd, const uint16_t* dres, int64_t M, int64_t K, uint16_t* dx,
+                               float* dweight, void* workspace, hipStream_t stream);
+
+// Norm of all values of `count` tensors (fp32 or bf16 by dtype[i]); with clip, the tensors scaled to
+// max_norm into `out` by the norm computed here or by *norm_in (then no workspace is needed).
+size_t grad_norm_workspace_size(int64_t count);
+hipError_t launch_grad_norm(int64_t count, const void* const* grads, void* const* out, const int64_t* n,
+                            const int32_t* dtype, bool clip, float max_norm, const float* norm_in,
+                            float* norm_out, void* workspace, hipStream_t stream);
+
+// ---- mixture of experts ----
+// Stable order of the T x J choices `ids` (64-bit with wide) by expert; workspace for many pairs.
+size_t expert_order_workspace_size(int64_t P, int64_t E);
+hipError_t launch_expert_order(const void* ids, int wide, int64_t T, int64_t J, int64_t E, int* rows,
+                               int* offsets, int* slots, void* workspace, hipStream_t stream);
+// out (T, D) = sum over J of w y[slots], and its backward (dw optional; w NULL: 1).
+hipError_t launch_combine(const uint16_t* y, const int* slots, const float* w, int64_t T, int64_t J,
+                          int64_t P, int64_t D, uint16_t* out, hipStream_t stream);
+hipError_t launch_combine_back(const uint16_t* dout, const uint16_t* y, const int* slots, const float* w,
+                               int64_t T, int64_t J, int64_t P, int64_t D, uint16_t* dy, float* dw,
+                               hipStream_t stream);
+// The product of P sorted rows with their experts' matrices (E of N[g] rows each), row p reading token
+// rows[p] of xq (rows NULL: token p; with rows, T * K fits 31 bits).
+hipError_t launch_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T, const int* rows,
+                               const int* offsets, int64_t P, int64_t E, int64_t K, int groups,
+                               const uint8_t* const* packed, const float* const* w_scale,
+                               const int64_t* N, void* const* out, int out_dtype, hipStream_t stream);
+// Codes and scales of the tokens rows[p]; zeros and 1 where there is no such token.
+hipError_t launch_gather_codes(const int8_t* xq, const float* a_scale, int64_t T, const int* rows, int64_t P,
+                               int64_t K, int8_t* out, float* out_scale, hipStream_t stream);
+// Its gradients; xq and a_scale of the weight gradient in the rows' order.
+hipError_t launch_grad_input_experts(const uint16_t* const* dy, const int* offsets, int64_t P, int64_t E,
+                                     const uint8_t* const* packed, const float* const* w_scale,
+                                     const int64_t* N, int groups, int64_t K, uint16_t* dx, hipStream_t stream);
+hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, const float* a_scale,
+                                      const int* offsets, int64_t P, int64_t E, int64_t N, int64_t K,
+                                      void* dw, int out_dtype, hipStream_t stream);
+
 }  // namespace bitnet

@@ -33,8 +33,6 @@ namespace bitnet {
 
 namespace {
 
-constexpr int kTeamGroups = 2;  // groups of V elements a lane holds
-
 struct NormArgs {
     const uint16_t* x;
     const float *w, *b;  // NULL: 1 and 0
@@ -46,19 +44,6 @@ struct NormArgs {
     int pow2;
     float *mean, *rstd;  // NULL: not written
 };
-
-template <int V>
-__device__ __forceinline__ void load_f32(const float* p, int64_t g, float missing, float (&v)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-        const float4 t = p ? reinterpret_cast<const float4*>(p)[(g * V + i) / 4]
-                           : make_float4(missing, missing, missing, missing);
-        v[i] = t.x;
-        v[i + 1] = t.y;
-        v[i + 2] = t.z;
-        v[i + 3] = t.w;
-    }
-}
 
 template <int V, int WPR>
 __global__ __launch_bounds__(64 * WPR) void layernorm_kernel(NormArgs p) {
@@ -209,42 +194,6 @@ struct NormBackArgs {
     uint16_t* dx;
     float* part;  // (blocks, 2, K) column sums, NULL: not wanted
 };
-
-template <int V, bool CODES>
-struct XVec {
-    RowVec<V> v;
-};
-template <int V>
-struct XVec<V, true> {
-    uint32_t q[V / 4];
-};
-template <int V, bool CODES>
-__device__ __forceinline__ XVec<V, CODES> load_x(const void* x, int64_t row, int64_t g) {
-    XVec<V, CODES> r;
-    if constexpr (CODES) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const int8_t*>(x) + row) + g * (V / 4);
-        if constexpr (V == 8) {
-            const uint2 t = *reinterpret_cast<const uint2*>(p);
-            r.q[0] = t.x;
-            r.q[1] = t.y;
-        } else {
-            r.q[0] = *p;
-        }
-    } else {
-        r.v = load_row_vec<V>(static_cast<const uint16_t*>(x) + row, g);
-    }
-    return r;
-}
-// The bf16 values or the codes as fp32, exactly.
-template <int V, bool CODES>
-__device__ __forceinline__ void x_to_f32(const XVec<V, CODES>& v, float (&x)[V]) {
-    if constexpr (CODES) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = (float)(int8_t)(v.q[j / 4] >> (8 * (j & 3)));
-    } else {
-        to_f32<V>(v.v, x);
-    }
-}
 
 // xh = (x - mean) rstd, each step rounded relative to xh itself however far the row lies from
 // zero; from codes c = a x it is (c - a mean) (rstd / a), the difference in one fused
@@ -524,20 +473,6 @@ __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__
         for (int j = 0; j < P / 2; ++j) o.w[j] = f32x2_to_bf16x2_rne(f[2 * j] * inv, f[2 * j + 1] * inv);
         store_row_vec<P>(x + m * groups * V, g * (V / P) + i, o);
     }
-}
-
-// Waves per row whose lanes hold the row in two groups each; 0: too long.
-int team_waves(int64_t K, int V) {
-    for (int w = 1; w <= 16; w *= 2)
-        if (K <= (int64_t)w * 64 * kTeamGroups * V) return w;
-    return 0;
-}
-
-// Waves per row of the backward pass, one group a lane up to 16 waves, then two; 0: too long.
-int back_waves(int64_t K, int V) {
-    for (int w = 1; w <= 16; w *= 2)
-        if (K <= (int64_t)w * 64 * V) return w;
-    return K <= (int64_t)16 * 64 * 2 * V ? 16 : 0;
 }
 
 // Blocks of the backward pass.

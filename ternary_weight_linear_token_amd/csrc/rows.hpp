@@ -152,4 +152,71 @@ __device__ __forceinline__ void store_codes(int8_t* row, int64_t g, const RowVec
         reinterpret_cast<uint32_t*>(row)[g] = p[0];
 }
 
+constexpr int kTeamGroups = 2;  // groups of V elements a lane of a norm's team holds
+
+// V values of an fp32 vector, or `missing` where there is none.
+template <int V>
+__device__ __forceinline__ void load_f32(const float* p, int64_t g, float missing, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4 t = p ? reinterpret_cast<const float4*>(p)[(g * V + i) / 4]
+                           : make_float4(missing, missing, missing, missing);
+        v[i] = t.x;
+        v[i + 1] = t.y;
+        v[i + 2] = t.z;
+        v[i + 3] = t.w;
+    }
+}
+
+// V elements of a row that is bf16, or int8 codes.
+template <int V, bool CODES>
+struct XVec {
+    RowVec<V> v;
+};
+template <int V>
+struct XVec<V, true> {
+    uint32_t q[V / 4];
+};
+template <int V, bool CODES>
+__device__ __forceinline__ XVec<V, CODES> load_x(const void* x, int64_t row, int64_t g) {
+    XVec<V, CODES> r;
+    if constexpr (CODES) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const int8_t*>(x) + row) + g * (V / 4);
+        if constexpr (V == 8) {
+            const uint2 t = *reinterpret_cast<const uint2*>(p);
+            r.q[0] = t.x;
+            r.q[1] = t.y;
+        } else {
+            r.q[0] = *p;
+        }
+    } else {
+        r.v = load_row_vec<V>(static_cast<const uint16_t*>(x) + row, g);
+    }
+    return r;
+}
+// The bf16 values or the codes as fp32, exactly.
+template <int V, bool CODES>
+__device__ __forceinline__ void x_to_f32(const XVec<V, CODES>& v, float (&x)[V]) {
+    if constexpr (CODES) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = (float)(int8_t)(v.q[j / 4] >> (8 * (j & 3)));
+    } else {
+        to_f32<V>(v.v, x);
+    }
+}
+
+// Waves per row whose lanes hold the row in two groups each; 0: too long.
+inline int team_waves(int64_t K, int V) {
+    for (int w = 1; w <= 16; w *= 2)
+        if (K <= (int64_t)w * 64 * kTeamGroups * V) return w;
+    return 0;
+}
+
+// Waves per row of the backward pass, one group a lane up to 16 waves, then two; 0: too long.
+inline int back_waves(int64_t K, int V) {
+    for (int w = 1; w <= 16; w *= 2)
+        if (K <= (int64_t)w * 64 * V) return w;
+    return K <= (int64_t)16 * 64 * 2 * V ? 16 : 0;
+}
+
 }  // namespace bitnet
