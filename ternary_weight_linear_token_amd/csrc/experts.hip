@@ -6,7 +6,7 @@
 // Two kernels.  What bounds the product is the bytes of the weights of the experts that have rows,
 // while an expert has few, and the int8 matrix cores after that.
 //  * expert_stream_kernel (a few rows for each expert): a block takes 16 rows of one expert times
-//    16 NB rows of its weights and all of K, its waves interleaved 256-weight chunks of it; both
+//    64 rows of its weights and all of K, its waves interleaved 256-weight chunks of it; both
 //    operands go straight from memory into registers.
 //  * expert_tile_kernel: BM x BN tiles on v_mfma_i32_32x32x32_i8.  Activations pass through LDS
 //    (two stages, transposed in groups of 4 x 4 bytes, 16-byte chunks XOR-swizzled by row so that
@@ -113,24 +113,29 @@ __device__ __forceinline__ int token_of(const ExpertArgs& p, const Unit& u, int 
 }
 
 // ------------------------------------------------------------------------------ tiles
-template <int BM, int BN, int WM, int WN, int W, bool ALIGNED>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), W) void expert_tile_kernel(ExpertArgs p) {
-    constexpr int TH = 64 * (BM / WM) * (BN / WN);
+template <int BM, int BN, int WM, int WN, int G, int D, int W, bool ALIGNED>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile_kernel(ExpertArgs p) {
+    constexpr int WPG = (BM / WM) * (BN / WN), TH = 64 * WPG;  // waves, threads of a group
     constexpr int MB = WM / 32, NB = WN / 32;
     constexpr int BK = 128, KS = BK / 32;  // a stage, and 32-k products of it
     constexpr int NA = BM * (BK / 16) / TH;  // 16-byte chunks of activations per thread and stage
     static_assert(NA >= 1 && NA * TH == BM * (BK / 16), "chunks");
     static_assert(TH % (BK / 16) == 0, "a thread keeps its chunk column");
-    __shared__ __align__(1024) uint8_t lds[2][BM * BK];
+    constexpr int kStage = BM * BK, kSums = WPG * MB * NB * 16 * 64 * 4;  // bytes of a stage; of a group's sums
+    constexpr int kLds = G * (2 * kStage > kSums && G > 1 ? 2 * kStage : (G > 1 ? kSums : 2 * kStage));
+    __shared__ __align__(1024) uint8_t smem[kLds];
     __shared__ float s_inva[BM];
 
     Unit u;
     if (!unit_of<BM, BN>(p, u)) return;
-    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, q = lane >> 5;
+    // G groups of waves share a tile: group g takes the stages g, g + G, ..; all run as many
+    const int g = G > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / TH) : 0;
+    const int tid = threadIdx.x - g * TH, lane = tid & 63, l32 = lane & 31, q = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / (BN / WN), wn = wave % (BN / WN);
     const int K = p.K, N = u.N, row_bytes = K / 4;
-    const int nsteps = (K + BK - 1) / BK;
+    const int nsteps = ((K + BK - 1) / BK + G - 1) / G;
+    uint8_t* const lds = smem + g * 2 * kStage;
 
     // ---- loads ----
     // Activations: thread tid takes chunk tid % 8 of rows tid / 8 + j TH / 8.  Gathered rows are
@@ -145,7 +150,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), W) void expert_tile_ker
         const int t = token_of(p, u, tid / (BK / 16) + j * (TH / (BK / 16)));
         voff_a[j] = t < 0 ? kOut : (uint32_t)((p.rows ? t : t - u.m0) * K + 16 * cc);
     }
-    for (int i = tid; i < BM; i += TH) {
+    for (int i = threadIdx.x; i < BM; i += TH * G) {
         const int t = token_of(p, u, i);
         s_inva[i] = t < 0 ? 0.0f : 1.0f / p.a_scale[t];
     }
@@ -162,24 +167,27 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), W) void expert_tile_ker
         voff_b[i] = row < rows_b ? (uint32_t)(row * row_bytes) + skew + 16 * q : kOut;
     }
 
-    u32x4 ar[NA], br[2][NB];
-    auto load_a = [&](int j, int step) {
-        const int k0 = step * BK;
+    // Activations are loaded D steps before they go to LDS, weights DB - 1 steps before their use.
+    constexpr int DB = D > 2 ? D : 2;
+    static_assert(D == 1 || D == 2 || D == 4, "sets go round with the stages");
+    u32x4 ar[D][NA], br[DB][NB];
+    auto load_a = [&](int set, int j, int step) {
+        const int k0 = (step * G + g) * BK;
         // a chunk behind the row's end reads zeros; soff 0 keeps kOut from wrapping
         const bool in = k0 + 16 * cc < K && voff_a[j] != kOut;
-        ar[j] = load16(ra, in ? voff_a[j] + k0 : kOut, 0);
+        ar[set][j] = load16(ra, in ? voff_a[j] + k0 : kOut, 0);
     };
     // the part of a chunk behind the row's end (K % 16 != 0)
-    auto mask_a = [&](int j, int step) {
+    auto mask_a = [&](int set, int j, int step) {
         if (!ALIGNED) {
-            const int left = K - step * BK - 16 * cc;  // bytes, a multiple of 4
+            const int left = K - (step * G + g) * BK - 16 * cc;  // bytes, a multiple of 4
 #pragma unroll
-            for (int d = 0; d < 4; ++d) ar[j][d] = left > 4 * d ? ar[j][d] : 0u;
+            for (int d = 0; d < 4; ++d) ar[set][j][d] = left > 4 * d ? ar[set][j][d] : 0u;
         }
     };
     auto load_b = [&](int set, int i, int step) {
         const bool in = step < nsteps && voff_b[i] != kOut;
-        const uint32_t off = in ? voff_b[i] + step * (BK / 4) : kOut;
+        const uint32_t off = in ? voff_b[i] + (step * G + g) * (BK / 4) : kOut;
         if (ALIGNED) {
             br[set][i] = load16(rb, off, 0);
         } else {
@@ -197,8 +205,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), W) void expert_tile_ker
 
     // Byte offset of chunk c of row r in a stage.
     auto at = [](int r, int c) { return r * BK + ((c ^ (r & 7)) << 4); };
-    auto store_a = [&](int j, uint8_t* s) {
-        const uint32_t d[4] = {ar[j][0], ar[j][1], ar[j][2], ar[j][3]};
+    auto store_a = [&](int set, int j, uint8_t* s) {
+        const uint32_t d[4] = {ar[set][j][0], ar[set][j][1], ar[set][j][2], ar[set][j][3]};
         uint32_t e[4];
         transpose4x4_bytes(d, e);
         *reinterpret_cast<uint4*>(s + at(tid / (BK / 16) + j * (TH / (BK / 16)), cc)) =
@@ -236,30 +244,37 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), W) void expert_tile_ker
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[j][i][r] = 0;
 
-    // Step it multiplies stage it % 2 and weight set it % 2, while the activations of step it + 1, in
-    // registers, go into the other stage and are loaded for step it + 2, and the other weight set
-    // is loaded for it + 1.  One barrier a step, before its last 32 k, whose operands are already
-    // in registers; the first operands of the next step are read behind it.
+    // Step it multiplies stage it % 2 and weight set it % DB, while the activations of step it + 1, in
+    // registers, go into the other stage and their registers are loaded for step it + 1 + D, and
+    // the weight set of step it - 1 for it + DB - 1.  One barrier a step, before its last 32 k, whose
+    // operands are already in registers; the first operands of the next step are read behind it.
     constexpr int NM = MB * NB, S = (KS - 1) * NM;  // slots; those before the barrier
-#pragma unroll
-    for (int j = 0; j < NA; ++j) load_a(j, 0);
 #pragma unroll
     for (int i = 0; i < NB; ++i) load_b(0, i, 0);
 #pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int j = 0; j < NA; ++j) load_a(d, j, d);
+#pragma unroll
+    for (int d = 1; d < DB - 1; ++d)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) load_b(d, i, d);
+#pragma unroll
     for (int j = 0; j < NA; ++j) {
-        mask_a(j, 0);
-        store_a(j, lds[0]);
-        load_a(j, 1);
+        mask_a(0, j, 0);
+        store_a(0, j, lds);
+        load_a(0, j, D);
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < MB; ++j) read(op[0], lds[0], 0, j);
+    for (int j = 0; j < MB; ++j) read(op[0], lds, 0, j);
 #pragma unroll
     for (int e = 0; e < 4 * NB; ++e) expand(op[0], br[0], 0, e);
-    auto step = [&](int it, auto set_c) {
-        constexpr int set = decltype(set_c)::value;
-        const uint8_t* const cur = lds[set];
-        uint8_t* const nxt = lds[set ^ 1];
+    auto step = [&](int it, auto at_c) {
+        constexpr int at = decltype(at_c)::value;  // it modulo the sets
+        constexpr int a_set = (at + 1) % D, b_set = at % DB, b_next = (at + 1) % DB, b_load = (at + DB - 1) % DB;
+        const uint8_t* const cur = lds + (at & 1) * kStage;
+        uint8_t* const nxt = lds + ((at & 1) ^ 1) * kStage;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const bool last = s == KS - 1;
@@ -271,89 +286,136 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), W) void expert_tile_ker
                 acc[m % MB][m / MB] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[m / MB], o.x[m % MB],
                                                                             acc[m % MB][m / MB], 0, 0, 0);
                 const int slot = s * NM + m;
-                if (slot < NB) load_b(set ^ 1, slot, it + 1);
+                if (slot < NB) load_b(b_load, slot, it + DB - 1);
 #pragma unroll
                 for (int j = 0; j < MB; ++j)
                     if (j * ((NM + 1) / 2) / MB == m) read(n, last ? nxt : cur, last ? 0 : s + 1, j);
 #pragma unroll
                 for (int e = 0; e < 4 * NB; ++e)
-                    if (NM / 2 + e * (NM - NM / 2) / (4 * NB) == m) expand(n, br[last ? set ^ 1 : set], last ? 0 : s + 1, e);
+                    if (NM / 2 + e * (NM - NM / 2) / (4 * NB) == m)
+                        expand(n, br[last ? b_next : b_set], last ? 0 : s + 1, e);
 #pragma unroll
                 for (int j = 0; j < NA; ++j)
                     if (j * S / NA + S / NA / 2 == slot) {
-                        mask_a(j, it + 1);
-                        store_a(j, nxt);
-                        load_a(j, it + 2);
+                        mask_a(a_set, j, it + 1);
+                        store_a(a_set, j, nxt);
+                        load_a(a_set, j, it + 1 + D);
                     }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
+    // whole rounds of the sets, then what is left (an exit inside the loop would give the
+    // accumulators a second live range)
     int it = 0;
-    for (; it + 2 <= nsteps; it += 2) {
+    for (; it + DB <= nsteps; it += DB) {
         step(it, std::integral_constant<int, 0>());
         step(it + 1, std::integral_constant<int, 1>());
+        if constexpr (DB > 2) {
+            step(it + 2, std::integral_constant<int, 2>());
+            step(it + 3, std::integral_constant<int, 3>());
+        }
     }
     if (it < nsteps) step(it, std::integral_constant<int, 0>());
+    if constexpr (DB > 2) {
+        if (it + 1 < nsteps) step(it + 1, std::integral_constant<int, 1>());
+        if (it + 2 < nsteps) step(it + 2, std::integral_constant<int, 2>());
+    }
 
-    // ---- outputs: lane (l32, q) of block (j, i) has row 32 j + l32, columns 32 i + 8 g + 4 q + 0 .. 3 ----
+    // ---- outputs: lane (l32, q) of block (j, i) has row 32 j + l32, columns 32 i + 8 c + 4 q + 0 .. 3 in
+    // registers 4 c ..; eight registers at a time (h: c = 2 h and 2 h + 1) ----
     const float* const ws = pick(p.w_scale, u.g) + (int64_t)u.e * N;
     void* const out = pick(p.out, u.g);
     const int dt = p.out_dtype;
     const bool wide = N % (dt == BITNET_OUT_BF16 ? 8 : 4) == 0;  // 16-byte aligned rows
+    auto scales = [&](int i, int h, float (&sc)[8]) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const int nb = u.n0 + wn * WN + 32 * i;
-        float sc[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int n = nb + 8 * (r >> 2) + 4 * q + (r & 3);
+        for (int r = 0; r < 8; ++r) {
+            const int n = u.n0 + wn * WN + 32 * i + 16 * h + 8 * (r >> 2) + 4 * q + (r & 3);
             sc[r] = n < N ? ws[n] : 0.0f;
         }
+    };
+    auto emit = [&](int j, int i, int h, const int (&v)[8], const float (&sc)[8]) {
+        const int nb = u.n0 + wn * WN + 32 * i + 16 * h;
+        const int ml = wm * WM + 32 * j + l32;
+        const bool live = ml < u.rows;
+        const float inv = s_inva[ml];
+        const int64_t o = (int64_t)(u.m0 + ml) * N + nb;
+        if (dt == BITNET_OUT_BF16 && wide && nb + 16 <= N) {
+            uint32_t b[4];
 #pragma unroll
-        for (int j = 0; j < MB; ++j) {
-            const int ml = wm * WM + 32 * j + l32;
-            const bool live = ml < u.rows;
-            const float inv = s_inva[ml];
-            const int64_t o = (int64_t)(u.m0 + ml) * N + nb;
-            if (dt == BITNET_OUT_BF16 && wide && nb + 32 <= N) {
-                uint32_t h[8];
+            for (int r = 0; r < 4; ++r)
+                b[r] = f32x2_to_bf16x2_rne(((float)v[2 * r] * sc[2 * r]) * inv,
+                                           ((float)v[2 * r + 1] * sc[2 * r + 1]) * inv);
+            // lanes l and l + 32 hold the halves of 8 columns: exchange, so that each has 8
+            const auto x = __builtin_amdgcn_permlane32_swap(b[0], b[2], false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(b[1], b[3], false, false);
+            if (live)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o + 8 * q) =
+                    make_uint4(x[0], y[0], x[1], y[1]);
+        } else if (live) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    h[r] = f32x2_to_bf16x2_rne(((float)acc[j][i][2 * r] * sc[2 * r]) * inv,
-                                               ((float)acc[j][i][2 * r + 1] * sc[2 * r + 1]) * inv);
-                // lanes l and l + 32 hold the halves of 8 columns: exchange, so that each has 8
+            for (int c = 0; c < 2; ++c) {
+                const int n = 8 * c + 4 * q;
+                if (dt != BITNET_OUT_BF16 && wide && nb + n + 4 <= N) {
+                    uint32_t x[4];
 #pragma unroll
-                for (int g = 0; g < 4; g += 2) {
-                    const auto a = __builtin_amdgcn_permlane32_swap(h[2 * g], h[2 * g + 2], false, false);
-                    const auto b = __builtin_amdgcn_permlane32_swap(h[2 * g + 1], h[2 * g + 3], false, false);
-                    if (live)
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o + 8 * (g + q)) =
-                            make_uint4(a[0], b[0], a[1], b[1]);
-                }
-            } else if (live) {
+                    for (int r = 0; r < 4; ++r)
+                        x[r] = dt == BITNET_OUT_I32
+                                   ? (uint32_t)v[4 * c + r]
+                                   : __float_as_uint(((float)v[4 * c + r] * sc[4 * c + r]) * inv);
+                    *reinterpret_cast<uint4*>(static_cast<uint32_t*>(out) + o + n) =
+                        make_uint4(x[0], x[1], x[2], x[3]);
+                } else {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int n = 8 * g + 4 * q;
-                    if (dt != BITNET_OUT_BF16 && wide && nb + n + 4 <= N) {
-                        uint4 v;
-                        if (dt == BITNET_OUT_I32)
-                            v = make_uint4((uint32_t)acc[j][i][4 * g], (uint32_t)acc[j][i][4 * g + 1],
-                                           (uint32_t)acc[j][i][4 * g + 2], (uint32_t)acc[j][i][4 * g + 3]);
-                        else
-                            v = make_uint4(__float_as_uint(((float)acc[j][i][4 * g] * sc[4 * g]) * inv),
-                                           __float_as_uint(((float)acc[j][i][4 * g + 1] * sc[4 * g + 1]) * inv),
-                                           __float_as_uint(((float)acc[j][i][4 * g + 2] * sc[4 * g + 2]) * inv),
-                                           __float_as_uint(((float)acc[j][i][4 * g + 3] * sc[4 * g + 3]) * inv));
-                        *reinterpret_cast<uint4*>(static_cast<uint32_t*>(out) + o + n) = v;
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (nb + n + r < N)
-                                store_out(out, o + n + r, dt, acc[j][i][4 * g + r], sc[4 * g + r], inv);
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        if (nb + n + r < N) store_out(out, o + n + r, dt, v[4 * c + r], sc[4 * c + r], inv);
                 }
             }
+        }
+    };
+    if constexpr (G == 1) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float sc[8];
+                scales(i, h, sc);
+#pragma unroll
+                for (int j = 0; j < MB; ++j) {
+                    int v[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) v[r] = acc[j][i][8 * h + r];
+                    emit(j, i, h, v, sc);
+                }
+            }
+    } else {
+        // every group leaves its sums in LDS and adds up, over the groups, the part it writes
+        constexpr int EV = MB * NB * 2;  // eighths of 16 registers
+        static_assert(EV % G == 0, "parts");
+        int* const sums = reinterpret_cast<int*>(smem);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    sums[((g * WPG + wave) * EV * 8 + (j * NB + i) * 16 + r) * 64 + lane] = acc[j][i][r];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < EV / G; ++e) {
+            const int ev = g * (EV / G) + e;  // uniform
+            int v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                v[r] = 0;
+#pragma unroll
+                for (int k = 0; k < G; ++k) v[r] += sums[((k * WPG + wave) * EV * 8 + ev * 8 + r) * 64 + lane];
+            }
+            float sc[8];
+            scales(ev / 2 % NB, ev & 1, sc);
+            emit(ev / 2 / NB, ev / 2 % NB, ev & 1, v, sc);
         }
     }
 }
@@ -361,14 +423,16 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), W) void expert_tile_ker
 // ----------------------------------------------------------------------- few rows
 constexpr int kStreamWaves = 4;
 
-// 16 rows of one expert times 16 NB weight rows and all of K (K % 16 == 0).  Wave w takes the
-// 256-weight chunks w, w + 4, ..; two batches of U chunks are in flight.
-template <int NB, int U>
-__global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(ExpertArgs p) {
-    constexpr int BN = 16 * NB;
-    __shared__ int red[kStreamWaves][NB * 4 * 64];
+// 16 rows of one expert times 64 rows of its weights and all of K (K % 16 == 0).  Wave w takes the
+// 256-weight chunks w, w + 4, ..; it has the weights of one chunk in flight, which come from memory,
+// and the activations of two halves of a chunk, which come from a cache: with few registers for
+// each, a CU holds the five blocks that hide both.
+__global__ __launch_bounds__(64 * kStreamWaves, 5) void expert_stream_kernel(ExpertArgs p) {
+    constexpr int NB = 4, BM = 16, BN = 16 * NB, TH = 64 * kStreamWaves;
+    constexpr int MO = BM * BN / TH;  // outputs of a thread
+    __shared__ int red[kStreamWaves][NB * 256];
     Unit u;
-    if (!unit_of<16, BN>(p, u)) return;
+    if (!unit_of<BM, BN>(p, u)) return;
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = p.K, N = u.N, row_bytes = K / 4;
@@ -380,90 +444,78 @@ __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(Expert
 #pragma unroll
     for (int i = 0; i < NB; ++i)  // rows behind the last one read zeros
         voff_b[i] = 16 * i + l16 < rows_b ? (uint32_t)((16 * i + l16) * row_bytes + 16 * q) : kOut;
-    const int token = token_of(p, u, l16);
-    const __amdgpu_buffer_rsrc_t ra =
-        p.rows ? rsrc(p.xq, (uint32_t)(p.T * K)) : rsrc(p.xq + (int64_t)u.m0 * K, (uint32_t)(u.rows * K));
-    const uint32_t voff_a = token < 0 ? kOut : (uint32_t)((p.rows ? token : token - u.m0) * K + 64 * q);
-    // the output pairs of this thread: scales asked for before the loop
-    const int nj = (nch - wave + kStreamWaves - 1) / kStreamWaves;
-
-    struct Chunk {
-        u32x4 w[NB], x[4];
-    };
-    auto load_w = [&](int j, Chunk& c) {
+    u32x4 w[NB];
+    auto load_w = [&](int j) {
         const int ch = wave + kStreamWaves * j;
 #pragma unroll
         for (int i = 0; i < NB; ++i)
-            c.w[i] = load16(rb, ch < nch && voff_b[i] != kOut ? voff_b[i] + 64 * ch : kOut, 0);
+            w[i] = load16(rb, ch < nch && voff_b[i] != kOut ? voff_b[i] + 64 * ch : kOut, 0);
     };
-    auto load_x = [&](int j, Chunk& c) {
+    load_w(0);
+    const __amdgpu_buffer_rsrc_t ra =
+        p.rows ? rsrc(p.xq, (uint32_t)(p.T * K)) : rsrc(p.xq + (int64_t)u.m0 * K, (uint32_t)(u.rows * K));
+    const int token = token_of(p, u, l16);
+    const uint32_t voff_a = token < 0 ? kOut : (uint32_t)((p.rows ? token : token - u.m0) * K + 64 * q);
+    u32x4 x[2][2];
+    auto load_x = [&](int j, int h) {  // half h of chunk j
         const int ch = wave + kStreamWaves * j;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const bool in = voff_a != kOut && 256 * ch + 64 * q + 16 * s < K;
-            c.x[s] = load16(ra, in ? voff_a + 256 * ch + 16 * s : kOut, 0);
+        for (int s = 0; s < 2; ++s) {
+            const int k = 256 * ch + 32 * h + 16 * s;
+            x[h][s] = load16(ra, voff_a != kOut && k + 64 * q < K ? voff_a + k : kOut, 0);
         }
     };
+    load_x(0, 0);
+    load_x(0, 1);
+    // scales of this thread's outputs, column tid % BN of rows tid / BN + i TH / BN
+    const int n = u.n0 + tid % BN;
+    const float ws = n < N ? pick(p.w_scale, u.g)[(int64_t)u.e * N + n] : 0.0f;
+    float scale[MO];
+#pragma unroll
+    for (int i = 0; i < MO; ++i) {
+        const int t = token_of(p, u, tid / BN + i * (TH / BN));
+        scale[i] = t < 0 ? 1.0f : p.a_scale[t];  // a row of zeros stays zero
+    }
     v4i acc[NB];
 #pragma unroll
     for (int i = 0; i < NB; ++i) acc[i] = v4i{0, 0, 0, 0};
-    auto compute = [&](const Chunk& c) {
+    const int nj = (nch - wave + kStreamWaves - 1) / kStreamWaves;
+    for (int j = 0; j < nj; ++j) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint32_t d[4] = {c.x[s][0], c.x[s][1], c.x[s][2], c.x[s][3]};
-            uint32_t e[4];
-            transpose4x4_bytes(d, e);
-            const v4i x = {(int)e[0], (int)e[1], (int)e[2], (int)e[3]};
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const uint32_t b = c.w[i][s];
-                const v4i w = {(int)ternary_field_i8<0>(b), (int)ternary_field_i8<1>(b),
-                               (int)ternary_field_i8<2>(b), (int)ternary_field_i8<3>(b)};
-                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, acc[i], 0, 0, 0);
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t d[4] = {x[h][s][0], x[h][s][1], x[h][s][2], x[h][s][3]};
+                uint32_t e[4];
+                transpose4x4_bytes(d, e);
+                const v4i a = {(int)e[0], (int)e[1], (int)e[2], (int)e[3]};
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const uint32_t b = w[i][2 * h + s];
+                    const v4i c = {(int)ternary_field_i8<0>(b), (int)ternary_field_i8<1>(b),
+                                   (int)ternary_field_i8<2>(b), (int)ternary_field_i8<3>(b)};
+                    acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, a, acc[i], 0, 0, 0);
+                }
             }
+            load_x(j + 1, h);
         }
-    };
-    Chunk a[U], b[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) load_w(k, a[k]);
-#pragma unroll
-    for (int k = 0; k < U; ++k) load_x(k, a[k]);
-    for (int j0 = 0; j0 < nj; j0 += 2 * U) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            load_w(j0 + U + k, b[k]);
-            load_x(j0 + U + k, b[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (j0 + k < nj) compute(a[k]);
-        if (j0 + U >= nj) break;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            load_w(j0 + 2 * U + k, a[k]);
-            load_x(j0 + 2 * U + k, a[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (j0 + U + k < nj) compute(b[k]);
+        load_w(j + 1);
     }
     // 16x16 accumulator: lane l, register r -> weight row 4 (l / 16) + r, token l % 16
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave][(16 * i + 4 * q + r) * 16 + l16] = acc[i][r];
+        for (int r = 0; r < 4; ++r) red[wave][(16 * i + 4 * q + r) * BM + l16] = acc[i][r];
     __syncthreads();
-    const float* const ws = pick(p.w_scale, u.g) + (int64_t)u.e * N;
     void* const out = pick(p.out, u.g);
-    for (int idx = tid; idx < BN * u.rows; idx += 64 * kStreamWaves) {
-        const int m = idx / BN, n = idx % BN;
-        if (n >= rows_b) continue;
+#pragma unroll
+    for (int i = 0; i < MO; ++i) {
+        const int m = tid / BN + i * (TH / BN);
+        if (m >= u.rows || n >= N) continue;
         int sum = 0;
 #pragma unroll
-        for (int w = 0; w < kStreamWaves; ++w) sum += red[w][n * 16 + m];
-        const int t = token_of(p, u, m);
-        store_out(out, (int64_t)(u.m0 + m) * N + u.n0 + n, p.out_dtype, sum, ws[u.n0 + n],
-                  t < 0 ? 0.0f : 1.0f / p.a_scale[t]);
+        for (int v = 0; v < kStreamWaves; ++v) sum += red[v][(tid % BN) * BM + m];
+        store_out(out, (int64_t)(u.m0 + m) * N + n, p.out_dtype, sum, ws, 1.0f / scale[i]);
     }
 }
 
@@ -534,17 +586,30 @@ hipError_t launch_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T
         a.w_scale[a.groups] = w_scale[g];
         a.out[a.groups++] = out[g];
     }
-    const int64_t per = P / (E < P ? E : P);  // rows of an expert, if they are spread evenly
+    // Rows of an expert and row tiles, if the rows are spread evenly; and the columns' tiles.
+    const int64_t active = E < P ? E : P, per = P / active;
+    int64_t cols = 0;
+    for (int g = 0; g < a.groups; ++g) cols += (a.N[g] + 127) / 128;
+    const int64_t units = active * ((per + 63) / 64) * cols;  // of 64 x 128
     const bool aligned = K % 16 == 0;
-    if (aligned && per <= 16) return launch_units(expert_stream_kernel<2, 2>, a, 16, 32, 64 * kStreamWaves, 1, stream);
-    if (per <= 64)
-        return aligned ? launch_units(expert_tile_kernel<64, 128, 64, 32, 2, true>, a, 64, 128, 256, 2, stream)
-                       : launch_units(expert_tile_kernel<64, 128, 64, 32, 2, false>, a, 64, 128, 256, 2, stream);
-    if (per <= 192)
-        return aligned ? launch_units(expert_tile_kernel<128, 128, 64, 64, 2, true>, a, 128, 128, 256, 4, stream)
-                       : launch_units(expert_tile_kernel<128, 128, 64, 64, 2, false>, a, 128, 128, 256, 4, stream);
-    return aligned ? launch_units(expert_tile_kernel<256, 256, 128, 64, 2, true>, a, 256, 256, 512, 4, stream)
-                   : launch_units(expert_tile_kernel<256, 256, 128, 64, 2, false>, a, 256, 256, 512, 4, stream);
+    // Few rows: the stream re-reads the activations for every 64 weight rows, 64 x 128 tiles keep
+    // them in LDS but need two blocks on a CU to hide their steps' latency.  Four rows each of 64 experts
+    // (640 x 2560, twice) 15.2 us against 19.5, 16 rows 29.3 against 24.9; four rows each of 8 experts
+    // (4096 x 14336: 256 tiles of 112 steps) 31 against 62.
+    if (aligned && (per <= 4 || (per <= 16 && units < 512)))
+        return launch_units(expert_stream_kernel, a, 16, 64, 64 * kStreamWaves, 1, stream);
+    // 128 x 256 from about a hundred rows on: 512 rows each of 8 experts (14336 x 4096, twice) 490 us
+    // against 621 in 64 x 128 tiles and 559 in 256 x 256 ones, of which a quarter is padding and one
+    // block fills a CU; 128 rows 177 against 203; 64 rows 43 (6912 x 2560) either way.
+    if (per >= 96)
+        return aligned ? launch_units(expert_tile_kernel<128, 256, 128, 64, 1, 1, 2, true>, a, 128, 256, 256, 4, stream)
+                       : launch_units(expert_tile_kernel<128, 256, 128, 64, 1, 1, 2, false>, a, 128, 256, 256, 4, stream);
+    // Too few tiles for two blocks on a CU: two groups of waves share the steps of each.  32 rows each of
+    // 8 experts (4096 x 14336) 71 us against 81; 32 rows of 64 (2560 x 640) 26 against 21.
+    if (aligned && units < 512)
+        return launch_units(expert_tile_kernel<64, 128, 64, 32, 2, 1, 4, true>, a, 64, 128, 512, 2, stream);
+    return aligned ? launch_units(expert_tile_kernel<64, 128, 64, 32, 1, 1, 4, true>, a, 64, 128, 256, 2, stream)
+                   : launch_units(expert_tile_kernel<64, 128, 64, 32, 1, 1, 4, false>, a, 64, 128, 256, 2, stream);
 }
 
 hipError_t launch_gather_codes(const int8_t* xq, const float* a_scale, int64_t T, const int* rows, int64_t P,

@@ -43,14 +43,20 @@ template <int BM>
 struct ExpertTiles {
     const int* offsets;
     int E, P, per, sum, scan;
-    int total;  // uniform
+    ExpertRows mine;  // of the lane's expert, with one expert a lane
+    int total;        // uniform
 
     __device__ __forceinline__ ExpertTiles(const int* off, int experts, int rows)
-        : offsets(off), E(experts), P(rows), per((experts + 63) >> 6), sum(0) {
+        : offsets(off), E(experts), P(rows), per((experts + 63) >> 6), sum(0), mine{0, 0} {
         const int lane = threadIdx.x & 63;
-        for (int i = 0; i < per; ++i) {
-            const int e = lane * per + i;
-            if (e < E) sum += (expert_rows(offsets, e, P).count + BM - 1) / BM;
+        if (per == 1) {
+            if (lane < E) mine = expert_rows(offsets, lane, P);
+            sum = (mine.count + BM - 1) / BM;
+        } else {
+            for (int i = 0; i < per; ++i) {
+                const int e = lane * per + i;
+                if (e < E) sum += (expert_rows(offsets, e, P).count + BM - 1) / BM;
+            }
         }
         scan = wave_scan(sum);
         total = __builtin_amdgcn_readlane(scan, 63);
@@ -61,17 +67,18 @@ struct ExpertTiles {
         const uint64_t past = __ballot(scan > t);
         const int l = (int)__builtin_ctzll(past);
         int left = t - (__builtin_amdgcn_readlane(scan, l) - __builtin_amdgcn_readlane(sum, l));
+        ExpertRows r = {__builtin_amdgcn_readlane(mine.first, l), __builtin_amdgcn_readlane(mine.count, l)};
         e = l * per;
-        for (;; ++e) {
-            const ExpertRows r = expert_rows(offsets, e, P);
-            const int n = (r.count + BM - 1) / BM;
-            if (left < n || e == E - 1) {
-                first = r.first + left * BM;
-                rows = min(BM, r.count - left * BM);
-                return;
+        if (per > 1) {
+            for (;; ++e) {
+                r = expert_rows(offsets, e, P);
+                const int n = (r.count + BM - 1) / BM;
+                if (left < n || e == E - 1) break;
+                left -= n;
             }
-            left -= n;
         }
+        first = r.first + left * BM;
+        rows = min(BM, r.count - left * BM);
     }
 };
 

@@ -178,15 +178,23 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     int tiles_i = p.tiles_i;
     std::conditional_t<EXPERTS && MODE == 1, ExpertTiles<BM>, NoTiles> rows_of(p.offsets, p.E, p.P);
     if constexpr (EXPERTS && MODE == 1) tiles_i = rows_of.total;
-    const int tiles = tiles_i * p.tiles_j, total = tiles * (EXPERTS ? (MODE == 0 ? p.E : 1) : p.slices);
-    int t = blockIdx.x;
-    {
+    const int tiles = tiles_i * p.tiles_j;
+    int t = blockIdx.x, slice;  // EXPERTS, MODE 0: the expert
+    if constexpr (EXPERTS && MODE == 0) {
+        // every XCD takes an eighth of each expert's tiles: a run of whole experts would leave the
+        // XCD with the most rows working alone (8 experts of 6912 x 2560, 4096 rows: 900 -> 320 us)
+        const int xcd = t & 7, b = t >> 3, share = (tiles + 7) >> 3;
+        slice = b / share;
+        t = xcd * share + (b - slice * share);
+        if (t >= tiles) return;
+    } else {
+        const int total = tiles * (EXPERTS ? 1 : p.slices);
         const int xcd = t & 7, q = total >> 3, r = total & 7;
         if (EXPERTS && (t >> 3) >= q + (xcd < r ? 1 : 0)) return;  // fewer tiles than there might be
         t = xcd * q + (xcd < r ? xcd : r) + (t >> 3);
+        slice = t / tiles;
+        t -= slice * tiles;
     }
-    const int slice = t / tiles;  // EXPERTS, MODE 0: the expert
-    t -= slice * tiles;
     constexpr int kPanel = 4;
     const int panel = t / (kPanel * p.tiles_j);
     const int ph = tiles_i - panel * kPanel < kPanel ? tiles_i - panel * kPanel : kPanel;
@@ -720,9 +728,8 @@ constexpr GradCfg kCfg[] = {
 constexpr int kCfgs = sizeof(kCfg) / sizeof(kCfg[0]);
 constexpr int kCUs = 256;
 
-// The configuration and number of slices with the least estimated time, of `copies` such products
-// (experts, each unsplit) in one launch.
-GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups, int64_t copies = 0) {
+// The configuration and number of slices with the least estimated time.
+GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups) {
     GradPlan best = {0, 1, 0};
     double best_t = 1e300;
     for (int c = 0; c < kCfgs; ++c) {
@@ -730,8 +737,8 @@ GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups, int6
         if (k.mode != mode) continue;
         int64_t steps = 0;
         for (int q = 0; q < groups; ++q) steps += (L[q] + k.bl - 1) / k.bl;
-        const int64_t tiles = ((I + k.bm - 1) / k.bm) * ((J + k.bn - 1) / k.bn) * (copies > 0 ? copies : 1);
-        for (int64_t s = 1; s <= (copies > 0 ? 1 : 16); ++s) {
+        const int64_t tiles = ((I + k.bm - 1) / k.bm) * ((J + k.bn - 1) / k.bn);
+        for (int64_t s = 1; s <= 16; ++s) {
             // at least two steps per group of a slice, at most 64 MB of partial sums
             if (s > 1 && (steps < 2 * s * k.g || s * I * J * 4 > ((int64_t)64 << 20))) break;
             const double per = (double)(((steps + s - 1) / s + k.g - 1) / k.g);
@@ -753,12 +760,12 @@ GradPlan plan(int mode, int64_t I, int64_t J, const int64_t* L, int groups, int6
     return best;
 }
 
-template <int C, Rows ROWS, bool EXPERTS = false>
+template <int C, Rows ROWS>
 void launch_rows(const GradArgs& a, hipStream_t stream) {
     constexpr GradCfg k = kCfg[C];
-    const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices + (EXPERTS ? 7 : 0)));
+    const dim3 grid((unsigned)((int64_t)a.tiles_i * a.tiles_j * a.slices));
     const dim3 block(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g);
-    hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, ROWS, EXPERTS>), grid,
+    hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, ROWS, false>), grid,
                        block, 0, stream, a);
 }
 
@@ -770,36 +777,6 @@ void launch_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
         launch_rows<C, kCfg[C].mode == 0 ? kOddEnd : kOdd>(a, stream);
     else
         launch_rows<C, kOdd>(a, stream);
-}
-
-template <int C>
-void launch_experts_cfg(const GradArgs& a, bool aligned, hipStream_t stream) {
-    if (aligned)
-        launch_rows<C, kWhole, true>(a, stream);
-    else
-        launch_rows<C, kCfg[C].mode == 0 ? kOddEnd : kOdd, true>(a, stream);
-}
-
-template <size_t... C>
-void launch_experts_any(int cfg, const GradArgs& a, bool aligned, hipStream_t stream, std::index_sequence<C...>) {
-    ((cfg == (int)C ? launch_experts_cfg<(int)C>(a, aligned, stream) : (void)0), ...);
-}
-
-// I and L of a are all rows (MODE 1: I, MODE 0: L[0]); the plan is that of rows spread evenly.
-hipError_t launch_grad_experts(int mode, GradArgs a, const int64_t* L, bool aligned, hipStream_t stream) {
-    const int64_t active = a.E < a.P ? a.E : a.P;
-    const int64_t even = active > 0 ? (a.P + active - 1) / active : 0;
-    const GradPlan pl = mode == 0 ? plan(0, a.I, a.J, &even, 1, a.E) : plan(1, even, a.J, L, a.groups, active);
-    const GradCfg& k = kCfg[pl.cfg];
-    const int64_t ti = mode == 0 ? (a.I + k.bm - 1) / k.bm : expert_tiles(a.P, a.E, k.bm);
-    const int64_t tj = (a.J + k.bn - 1) / k.bn, blocks = ti * tj * (mode == 0 ? a.E : 1);
-    if (blocks + 7 > max_blocks(64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g)) return hipErrorInvalidValue;
-    a.tiles_i = (int)ti;
-    a.tiles_j = (int)tj;
-    a.steps = pl.steps;
-    a.slices = mode == 0 ? a.E : 1;
-    launch_experts_any(pl.cfg, a, aligned, stream, std::make_index_sequence<kCfgs>());
-    return hipGetLastError();
 }
 
 template <size_t... C>
@@ -826,6 +803,38 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
     if (e != hipSuccess || pl.slices == 1) return e;
     hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream,
                        a.part, a.slices, n, a.out_dtype, a.out);
+    return hipGetLastError();
+}
+
+// ---- grouped by expert ----
+// Tiles of the experts' gradients (mode, bm, bn, wm, wn, g, bl, d, w).  An expert brings few rows,
+// and with many of them there are tiles enough, so none is split and the tiles are smaller than
+// those of one large product.  dw: two blocks of 256 x 128 on a CU, one computing while the other
+// writes its outputs (8 experts of 6912 x 2560, 4096 rows, fp32: 227 us; 256 x 256 240, 128 x 128 260;
+// 16 of 641 x 2564, 258 rows: 22, 30 and 30).  dx: 64 x 256, whose rows are padded little and converted for
+// 256 columns at once (the first of these: 158 us; 64 x 128 190, 128 x 128 185, 256 x 256 190); below two
+// blocks for each CU 32 x 128 with four groups of waves (the second: 14 us against 24; 64 rows of 8 experts
+// of 6912 x 2560 34 against 92).
+constexpr GradCfg kExpertCfg[] = {
+    {0, 256, 128, 128, 64, 1, 32, 1, 2, 2, 0, 0, 0},
+    {1, 64, 256, 64, 64, 1, 64, 1, 2, 3, 0, 0, 0},
+    {1, 32, 128, 32, 64, 4, 64, 1, 2, 1, 0, 0, 0},
+};
+
+template <int C, Rows ROWS>
+hipError_t launch_experts(GradArgs a, hipStream_t stream) {
+    constexpr GradCfg k = kExpertCfg[C];
+    constexpr int threads = 64 * (k.bm / k.wm) * (k.bn / k.wn) * k.g;
+    const int64_t ti = k.mode == 0 ? (a.I + k.bm - 1) / k.bm : expert_tiles(a.P, a.E, k.bm);
+    const int64_t tj = (a.J + k.bn - 1) / k.bn;
+    // MODE 0: the tiles of an expert in eighths, one for each XCD
+    const int64_t blocks = (ti * tj + 7) / 8 * 8 * (k.mode == 0 ? a.E : 1);
+    if (blocks > max_blocks(threads)) return hipErrorInvalidValue;
+    a.tiles_i = (int)ti;
+    a.tiles_j = (int)tj;
+    for (int q = 0; q < a.groups; ++q) a.steps += (a.L[q] + k.bl - 1) / k.bl;  // MODE 1
+    hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, ROWS, true>),
+                       dim3((unsigned)blocks), dim3(threads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -894,15 +903,13 @@ hipError_t launch_grad_input_experts(const uint16_t* const* dy, const int* offse
                                      const uint8_t* const* packed, const float* const* w_scale,
                                      const int64_t* N, int groups, int64_t K, uint16_t* dx, hipStream_t stream) {
     GradArgs a = {};
-    int64_t L[BITNET_MAX_GROUPS] = {};
     bool aligned = K % 16 == 0;
     for (int q = 0; q < groups; ++q) {
         if (N[q] == 0) continue;  // adds nothing
         a.dy[a.groups] = dy[q];
         a.b[a.groups] = packed[q];
         a.scale[a.groups] = w_scale[q];
-        a.L[a.groups] = (int)N[q];
-        L[a.groups++] = N[q];
+        a.L[a.groups++] = (int)N[q];
         aligned = aligned && N[q] % 8 == 0;
     }
     a.I = (int)P;
@@ -912,7 +919,10 @@ hipError_t launch_grad_input_experts(const uint16_t* const* dy, const int* offse
     a.offsets = offsets;
     a.E = (int)E;
     a.P = (int)P;
-    return launch_grad_experts(1, a, L, aligned, stream);
+    const int64_t active = E < P ? E : P;
+    const int64_t units = active * ((P / active + 63) / 64) * ((K + 255) / 256);  // of 64 x 256, spread evenly
+    if (units >= 512) return aligned ? launch_experts<1, kWhole>(a, stream) : launch_experts<1, kOdd>(a, stream);
+    return aligned ? launch_experts<2, kWhole>(a, stream) : launch_experts<2, kOdd>(a, stream);
 }
 
 hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, const float* a_scale,
@@ -931,7 +941,7 @@ hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, cons
     a.offsets = offsets;
     a.E = (int)E;
     a.P = (int)P;
-    return launch_grad_experts(0, a, nullptr, N % 2 == 0, stream);
+    return N % 2 == 0 ? launch_experts<0, kWhole>(a, stream) : launch_experts<0, kOddEnd>(a, stream);
 }
 
 }  // namespace bitnet

@@ -24,7 +24,7 @@ namespace bitnet {
 namespace {
 
 constexpr int kOrderWaves = 8;
-constexpr int64_t kOrderChunk = 8192;  // fewest pairs of a block where there are several
+constexpr int64_t kOrderChunk = 1024;  // fewest pairs of a block where there are several
 constexpr int64_t kOrderBlocks = 256;
 constexpr int kBins = BITNET_MAX_EXPERTS + 1;  // the last bin in use is that of the dropped pairs
 

@@ -109,7 +109,7 @@ def check_forward(xq, a, counts, packed, s, rows, what, dts=("i32", "f32", "bf16
 
 SHAPES = [(1, 2, 16, 16), (2, 8, 33, 64), (5, 3, 640, 2560), (16, 64, 40, 256), (40, 4, 130, 260),
           (100, 16, 641, 2564), (256, 64, 640, 2560), (300, 3, 257, 1028), (700, 8, 300, 4096), (999, 5, 512, 132),
-          (1500, 2, 256, 272), (2100, 8, 2560, 640), (600, 1, 256, 1024), (129, 200, 17, 20), (64, 1024, 8, 80)]
+          (1500, 2, 256, 272), (2100, 8, 2560, 640), (600, 1, 256, 1024), (129, 200, 17, 20), (64, 1024, 8, 80), (1500, 64, 1100, 272), (1500, 64, 1100, 276)]
 
 
 @pytest.mark.parametrize("P,E,N,K", SHAPES)
@@ -221,7 +221,7 @@ def test_outputs_past_32_bits():
 
 GRADS = [(1, 2, 1, 4), (3, 2, 17, 20), (5, 3, 640, 2560), (40, 4, 63, 252), (100, 16, 641, 2564), (300, 3, 257, 1028),
          (700, 8, 300, 516), (999, 5, 130, 260), (1200, 2, 256, 256), (4100, 4, 33, 64), (258, 64, 64, 640),
-         (2100, 2, 2560, 512), (90, 200, 6, 20), (513, 4, 128, 4112)]
+         (2100, 2, 2560, 512), (90, 200, 6, 20), (513, 4, 128, 4112), (1500, 64, 40, 2064), (1500, 64, 33, 2052)]
 
 
 @pytest.mark.parametrize("P,E,N,K", GRADS)
