@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from array import array
 
 import torch
 
@@ -873,18 +874,23 @@ _GRAD_CODES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 
 def _grad_list(tensors, name, device):
     """Host arrays (pointers, sizes, types) of a list of fp32 and bf16 tensors on one device."""
-    ptrs, sizes, codes = [], [], []
+    index, codes = device.index, []
     for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}[{i}] must be a torch.Tensor")
-        code = _GRAD_CODES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{name}[{i}] must be torch.float32 or torch.bfloat16, got {t.dtype}")
-        ptrs.append(_arg(t, t.dtype, f"{name}[{i}]", None, device))
-        sizes.append(t.numel())
+        code = _GRAD_CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+        if code is None or type(t) is not torch.Tensor or t.get_device() != index or not t.is_contiguous(
+                ) or t.requires_grad:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}[{i}] must be a torch.Tensor")
+            if code is None:
+                raise TypeError(f"{name}[{i}] must be torch.float32 or torch.bfloat16, got {t.dtype}")
+            _arg(t, t.dtype, f"{name}[{i}]", None, device)  # raises what is wrong, or takes a subclass
         codes.append(code)
-    n = len(ptrs)
-    return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*codes))
+    return (array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]),
+            array("i", codes))
+
+
+def _address(a):
+    return a.buffer_info()[0]
 
 
 def _grad_device(grads):
@@ -908,8 +914,8 @@ def grad_norm(grads, out=None, workspace=None):
         out = torch.empty((), dtype=torch.float32, device=d)
     need = int(lib().bitnet_grad_norm_workspace_size(len(grads))) if workspace is None else 0
     ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
-    _run("bitnet_grad_norm", d, len(grads), P, N, T, _arg(out, torch.float32, "out", (), d), ws_ptr,
-         ws_bytes)
+    _run("bitnet_grad_norm", d, len(grads), _address(P), _address(N), _address(T),
+         _arg(out, torch.float32, "out", (), d), ws_ptr, ws_bytes)
     return out
 
 
@@ -926,15 +932,20 @@ def clip_grads(grads, max_norm, norm=None, out=None, workspace=None):
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must have one tensor per gradient")
-        O = (ctypes.c_void_p * len(out))(*[_arg(o, g.dtype, f"out[{i}]", tuple(g.shape), d)
-                                           for i, (o, g) in enumerate(zip(out, grads))])
+        O = _grad_list(out, "out", d)[0]
+        for i, (o, g) in enumerate(zip(out, grads)):
+            if o.shape != g.shape:
+                raise ValueError(f"out[{i}] has shape {tuple(o.shape)}, expected {tuple(g.shape)}")
+            if o.dtype is not g.dtype:
+                raise TypeError(f"out[{i}] must be {g.dtype}, got {o.dtype}")
     ws_ptr, ws_bytes, ws = None, 0, None
     norm_in = _arg(norm, torch.float32, "norm", (), d)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=d)
         need = int(lib().bitnet_grad_norm_workspace_size(len(grads))) if workspace is None else 0
         ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
-    _run("bitnet_clip_grads", d, len(grads), P, O, N, T, float(max_norm), norm_in,
+    _run("bitnet_clip_grads", d, len(grads), _address(P), _address(O), _address(N), _address(T),
+         float(max_norm), norm_in,
          norm.data_ptr() if norm_in is None else None, ws_ptr, ws_bytes)
     return norm
 

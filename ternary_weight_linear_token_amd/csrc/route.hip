@@ -98,10 +98,26 @@ __global__ __launch_bounds__(64 * kOrderWaves) void order_count_kernel(OrderArgs
 
 __global__ __launch_bounds__(64 * kOrderWaves) void order_kernel(OrderArgs a) {
     __shared__ int hist[kOrderWaves][kBins];  // then the next row of each wave and bin
+    __shared__ int s_total[kBins], s_before[kBins];  // of all blocks, of the earlier ones
     __shared__ int s_wave[kOrderWaves];
     constexpr int kThreads = 64 * kOrderWaves;
     const int bits = bits_of(a.E), tid = threadIdx.x;
+    const bool alone = gridDim.x == 1;
+    if (!alone)
+        for (int e = tid; e <= a.E; e += kThreads) s_total[e] = s_before[e] = 0;
     count(a, bits, hist);
+    if (!alone) {
+        // the counts of all blocks in one run of loads (integers: any order of the additions)
+        const int bins = a.E + 1, n = (int)gridDim.x * bins, mine = (int)blockIdx.x * bins;
+#pragma unroll 8
+        for (int i = tid; i < n; i += kThreads) {
+            const int c = a.counts[i], e = i % bins;
+            if (c == 0) continue;
+            atomicAdd(&s_total[e], c);
+            if (i < mine) atomicAdd(&s_before[e], c);
+        }
+        __syncthreads();
+    }
     // a thread takes bins per * tid ..: their totals, and how many of them lie in earlier blocks
     constexpr int per = (kBins + kThreads - 1) / kThreads;
     int total[per], before[per], sum = 0;
@@ -110,15 +126,12 @@ __global__ __launch_bounds__(64 * kOrderWaves) void order_kernel(OrderArgs a) {
         const int e = per * tid + i;
         total[i] = before[i] = 0;
         if (e <= a.E) {
-            if (gridDim.x == 1) {
+            if (alone) {
 #pragma unroll
                 for (int w = 0; w < kOrderWaves; ++w) total[i] += hist[w][e];
             } else {
-                for (int b = 0; b < (int)gridDim.x; ++b) {
-                    const int c = a.counts[(int64_t)b * (a.E + 1) + e];
-                    total[i] += c;
-                    if (b < (int)blockIdx.x) before[i] += c;
-                }
+                total[i] = s_total[e];
+                before[i] = s_before[e];
             }
         }
         sum += total[i];
