@@ -67,6 +67,23 @@ struct Unit {
     int g, n0, N;     // matrix, first weight row, weight rows of an expert
 };
 
+// Matrix and first weight row of column tile col of all matrices.
+template <int BN>
+__device__ __forceinline__ void column_of(const ExpertArgs& p, int col, Unit& u) {
+    u.g = 0;
+    u.N = p.N[0];
+#pragma unroll
+    for (int g = 1; g < BITNET_MAX_GROUPS; ++g)
+        if (g < p.groups && col >= p.tile[g]) {
+            u.g = g;
+            u.N = p.N[g];
+        }
+#pragma unroll
+    for (int g = 1; g < BITNET_MAX_GROUPS; ++g)
+        if (u.g == g) col -= p.tile[g];
+    u.n0 = col * BN;
+}
+
 // The block's unit.  Consecutive blocks go to different XCDs, so each XCD gets a contiguous run of
 // units; runs walk panels of p.panel row tiles column by column, so that an XCD's L2 holds the
 // panel's activations and the weights of few columns.
@@ -82,18 +99,7 @@ __device__ __forceinline__ bool unit_of(const ExpertArgs& p, Unit& u) {
     const uint32_t in = t - panel * per;
     int col = (int)(in / high);
     tiles.find((int)(panel * p.panel + in % high), u.e, u.m0, u.rows);
-    u.g = 0;
-    u.N = p.N[0];
-#pragma unroll
-    for (int g = 1; g < BITNET_MAX_GROUPS; ++g)
-        if (g < p.groups && col >= p.tile[g]) {
-            u.g = g;
-            u.N = p.N[g];
-        }
-#pragma unroll
-    for (int g = 1; g < BITNET_MAX_GROUPS; ++g)
-        if (u.g == g) col -= p.tile[g];
-    u.n0 = col * BN;
+    column_of<BN>(p, col, u);
     return true;
 }
 
@@ -431,8 +437,12 @@ __global__ __launch_bounds__(64 * kStreamWaves, 5) void expert_stream_kernel(Exp
     constexpr int NB = 4, BM = 16, BN = 16 * NB, TH = 64 * kStreamWaves;
     constexpr int MO = BM * BN / TH;  // outputs of a thread
     __shared__ int red[kStreamWaves][NB * 256];
+    // column tile x of row tile y: no block shares its weights, so which XCD takes it does not matter
     Unit u;
-    if (!unit_of<BM, BN>(p, u)) return;
+    const ExpertTiles<BM> tiles(p.offsets, p.E, p.P);
+    if ((int)blockIdx.y >= tiles.total) return;
+    column_of<BN>(p, (int)blockIdx.x, u);
+    tiles.find((int)blockIdx.y, u.e, u.m0, u.rows);
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = p.K, N = u.N, row_bytes = K / 4;
@@ -537,15 +547,21 @@ __global__ __launch_bounds__(256) void gather_codes_kernel(const int8_t* __restr
     if (g == 0) out_scale[p] = in ? a_scale[t] : 1.0f;
 }
 
-template <class KERNEL>
-hipError_t launch_units(KERNEL kernel, ExpertArgs a, int bm, int bn, int threads, int panel,
-                        hipStream_t stream) {
+// Column tiles of all matrices; their number goes to tile[].
+int64_t column_tiles(ExpertArgs& a, int bn) {
     int64_t tn = 0;
     for (int g = 0; g < BITNET_MAX_GROUPS; ++g) {
         a.tile[g] = (int)tn;
         if (g < a.groups) tn += (a.N[g] + bn - 1) / bn;
     }
     a.tile[BITNET_MAX_GROUPS] = (int)tn;
+    return tn;
+}
+
+template <class KERNEL>
+hipError_t launch_units(KERNEL kernel, ExpertArgs a, int bm, int bn, int threads, int panel,
+                        hipStream_t stream) {
+    const int64_t tn = column_tiles(a, bn);
     a.tiles_n = (int)tn;
     a.panel = panel;
     const int64_t units = expert_tiles(a.P, a.E, bm) * tn;
@@ -596,8 +612,13 @@ hipError_t launch_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T
     // them in LDS but need two blocks on a CU to hide their steps' latency.  Four rows each of 64 experts
     // (640 x 2560, twice) 15.2 us against 19.5, 16 rows 29.3 against 24.9; four rows each of 8 experts
     // (4096 x 14336: 256 tiles of 112 steps) 31 against 62.
-    if (aligned && (per <= 4 || (per <= 16 && units < 512)))
-        return launch_units(expert_stream_kernel, a, 16, 64, 64 * kStreamWaves, 1, stream);
+    if (aligned && (per <= 4 || (per <= 16 && units < 512))) {
+        const int64_t tn = column_tiles(a, 64), tm = expert_tiles(P, E, 16);  // at most 2048 row tiles
+        if (tn * tm > max_blocks(64 * kStreamWaves)) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(expert_stream_kernel, dim3((unsigned)tn, (unsigned)tm), dim3(64 * kStreamWaves), 0,
+                           stream, a);
+        return hipGetLastError();
+    }
     // 128 x 256 from about a hundred rows on: 512 rows each of 8 experts (14336 x 4096, twice) 490 us
     // against 621 in 64 x 128 tiles and 559 in 256 x 256 ones, of which a quarter is padding and one
     // block fills a CU; 128 rows 177 against 203; 64 rows 43 (6912 x 2560) either way.
