@@ -208,11 +208,12 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void rmsnorm_back_kernel(Rm
     const int64_t groups = p.K / V;
     const float inv_k = 1.0f / (float)p.K;
     float w[G][V], dw[G][V];
-    bool in[G];
+    bool in[G], some[G];  // of this lane, of this wave
 #pragma unroll
     for (int i = 0; i < G; ++i) {
         const int64_t g = lr + (int64_t)i * kStride;
         in[i] = g < groups;
+        some[i] = i == 0 || __builtin_amdgcn_readfirstlane((int)(__ballot(in[i]) != 0)) != 0;
         load_f32<V>(p.w, in[i] ? g : 0, 1.0f, w[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[i][j] = 0.0f;
@@ -251,6 +252,7 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void rmsnorm_back_kernel(Rm
         float z[G][V], g[G][V], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
+            if (!some[i]) continue;
             float d[V];
             to_f32<V>(cur.dy[i], d);
             x_to_f32<V, CODES>(cur.x[i], z[i]);
@@ -275,6 +277,7 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 512) void rmsnorm_back_kernel(Rm
         if (m < p.M) {
 #pragma unroll
             for (int i = 0; i < G; ++i) {
+                if (!some[i]) continue;
                 float r[V];
                 if (RES) to_f32<V>(cur.dres[RES ? i : 0], r);
                 RowVec<V> o;
@@ -447,7 +450,11 @@ hipError_t launch_rms_back_v(const RmsBackArgs& a, hipStream_t stream) {
         case 4: hipLaunchKernelGGL((rmsnorm_back_kernel<V, 4, 1, CODES, RES>), grid, dim3(512), 0, stream, a); break;
         case 8: hipLaunchKernelGGL((rmsnorm_back_kernel<V, 8, 1, CODES, RES>), grid, dim3(512), 0, stream, a); break;
         case 16:
-            if (a.K <= (int64_t)16 * 64 * V)
+            // two groups a lane with 16 waves fill a CU with one block; eight waves with three leave
+            // room for two (8191 x 4100 from a checkpoint: 57 -> 40 us)
+            if (V == 4 && a.K > (int64_t)16 * 64 * V && a.K <= (int64_t)8 * 64 * 3 * V)
+                hipLaunchKernelGGL((rmsnorm_back_kernel<V, 8, 3, CODES, RES>), grid, dim3(512), 0, stream, a);
+            else if (a.K <= (int64_t)16 * 64 * V)
                 hipLaunchKernelGGL((rmsnorm_back_kernel<V, 16, 1, CODES, RES>), grid, dim3(1024), 0, stream, a);
             else
                 hipLaunchKernelGGL((rmsnorm_back_kernel<V, 16, 2, CODES, RES>), grid, dim3(1024), 0, stream, a);

@@ -134,7 +134,7 @@ def check_back(dy, x, x64, w, rstd, x_scale, dres, what):
 
 @pytest.mark.parametrize("M,K", [(1, 4), (1, 2560), (3, 60), (33, 252), (7, 1028), (17, 2564), (40, 4096),
                                  (9, 8196), (5, 16384), (3, 16388), (2100, 512), (600, 2048), (1100, 8192),
-                                 (70, 20000)])
+                                 (70, 20000), (1100, 4100), (7, 6140), (5, 6148)])
 @pytest.mark.parametrize("ckpt", [False, True])
 @pytest.mark.parametrize("res", [False, True])
 def test_backward(M, K, ckpt, res):
