@@ -54,8 +54,14 @@ struct ExpertArgs {
     uint32_t first;  // first block of this launch
 };
 
+// Descriptor of a uniform range, in scalar registers wherever it was computed: in vector registers it
+// would put a loop over the lanes around every load.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)b) |
+                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)u, (short)0,
+                                             __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
@@ -97,7 +103,7 @@ __device__ __forceinline__ bool unit_of(const ExpertArgs& p, Unit& u) {
     const uint32_t per = (uint32_t)p.panel * (uint32_t)p.tiles_n, panel = t / per;
     const uint32_t high = min((uint32_t)p.panel, (uint32_t)tiles.total - panel * p.panel);
     const uint32_t in = t - panel * per;
-    int col = (int)(in / high);
+    const int col = (int)(in / high);
     tiles.find((int)(panel * p.panel + in % high), u.e, u.m0, u.rows);
     column_of<BN>(p, col, u);
     return true;
@@ -149,7 +155,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
     // ones from the tile's first.
     const int cc = tid % (BK / 16);
     const __amdgpu_buffer_rsrc_t ra =
-        p.rows ? rsrc(p.xq, (uint32_t)(p.T * K)) : rsrc(p.xq + (int64_t)u.m0 * K, (uint32_t)(u.rows * K));
+        rsrc(p.xq + (p.rows ? 0 : (int64_t)u.m0 * K), (uint32_t)((p.rows ? p.T : u.rows) * K));
     uint32_t voff_a[NA];
 #pragma unroll
     for (int j = 0; j < NA; ++j) {
@@ -463,7 +469,7 @@ __global__ __launch_bounds__(64 * kStreamWaves, 5) void expert_stream_kernel(Exp
     };
     load_w(0);
     const __amdgpu_buffer_rsrc_t ra =
-        p.rows ? rsrc(p.xq, (uint32_t)(p.T * K)) : rsrc(p.xq + (int64_t)u.m0 * K, (uint32_t)(u.rows * K));
+        rsrc(p.xq + (p.rows ? 0 : (int64_t)u.m0 * K), (uint32_t)((p.rows ? p.T : u.rows) * K));
     const int token = token_of(p, u, l16);
     const uint32_t voff_a = token < 0 ? kOut : (uint32_t)((p.rows ? token : token - u.m0) * K + 64 * q);
     u32x4 x[2][2];

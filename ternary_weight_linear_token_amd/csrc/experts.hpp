@@ -77,8 +77,10 @@ struct ExpertTiles {
                 left -= n;
             }
         }
-        first = r.first + left * BM;
-        rows = min(BM, r.count - left * BM);
+        // the same in every lane, and here in scalar registers
+        e = __builtin_amdgcn_readfirstlane(e);
+        first = __builtin_amdgcn_readfirstlane(r.first + left * BM);
+        rows = __builtin_amdgcn_readfirstlane(min(BM, r.count - left * BM));
     }
 };
 

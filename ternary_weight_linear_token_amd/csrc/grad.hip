@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
         // every XCD takes an eighth of each expert's tiles: a run of whole experts would leave the
         // XCD with the most rows working alone (8 experts of 6912 x 2560, 4096 rows: 900 -> 320 us)
         const int xcd = t & 7, b = t >> 3, share = (tiles + 7) >> 3;
-        slice = b / share;
+        slice = __builtin_amdgcn_readfirstlane(b / share);
         t = xcd * share + (b - slice * share);
         if (t >= tiles) return;
     } else {
@@ -199,7 +199,11 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     const int panel = t / (kPanel * p.tiles_j);
     const int ph = tiles_i - panel * kPanel < kPanel ? tiles_i - panel * kPanel : kPanel;
     const int tp = t - panel * kPanel * p.tiles_j;
-    const int ti = panel * kPanel + tp % ph, tj = tp / ph;
+    int ti = panel * kPanel + tp % ph, tj = tp / ph;
+    if constexpr (EXPERTS) {
+        ti = __builtin_amdgcn_readfirstlane(ti);
+        tj = __builtin_amdgcn_readfirstlane(tj);
+    }
     const int j0 = tj * BN, J = p.J;
     int i0 = ti * BM, I = p.I, expert = 0, row0 = 0, L = p.L[0], first_step = 0, steps = 0;
     if constexpr (!EXPERTS) {
@@ -208,8 +212,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     } else if constexpr (MODE == 0) {
         expert = slice;
         const ExpertRows r = expert_rows(p.offsets, expert, p.P);
-        row0 = r.first;
-        L = r.count;
+        row0 = __builtin_amdgcn_readfirstlane(r.first);  // into scalar registers, as the descriptors
+        L = __builtin_amdgcn_readfirstlane(r.count);
         steps = (L + BL - 1) / BL;
     } else {
         int rows;
