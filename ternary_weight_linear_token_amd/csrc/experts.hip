@@ -625,16 +625,23 @@ hipError_t launch_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T
                            stream, a);
         return hipGetLastError();
     }
-    // 128 x 256 from about a hundred rows on: 512 rows each of 8 experts (14336 x 4096, twice) 490 us
-    // against 621 in 64 x 128 tiles and 559 in 256 x 256 ones, of which a quarter is padding and one
-    // block fills a CU; 128 rows 177 against 203; 64 rows 43 (6912 x 2560) either way.
-    if (per >= 96)
-        return aligned ? launch_units(expert_tile_kernel<128, 256, 128, 64, 1, 1, 2, true>, a, 128, 256, 256, 4, stream)
-                       : launch_units(expert_tile_kernel<128, 256, 128, 64, 1, 1, 2, false>, a, 128, 256, 256, 4, stream);
+    // 128 x 256 where there are a hundred rows, one tile for every CU, and 32 steps or a thousand rows: 512
+    // rows each of 8 experts (14336 x 4096, twice) 491 us against 631 in 64 x 128 tiles and 559 in 256 x 256 ones, of
+    // which a quarter is padding and one block fills a CU; 256 rows (4096 x 14336) 167 against 182.  Fewer
+    // tiles: 434 rows of 3 experts (342 x 2432, twice) 38 against 14; fewer steps: 128 rows of 64
+    // (2560 x 640) 44 against 37, but 4096 rows of 4 (4096 x 1280) 115 against 135; columns off 16 (rows of 4-byte loads): 884 rows of 8 (2490 x 3592)
+    // 151 against 141.
+    int64_t wide = 0;
+    for (int g = 0; g < a.groups; ++g) wide += (a.N[g] + 255) / 256;
+    wide *= active * ((per + 127) / 128);
+    if (aligned && per >= 96 && wide >= 256 && (K >= 2048 || per >= 1024))
+        return launch_units(expert_tile_kernel<128, 256, 128, 64, 1, 1, 2, true>, a, 128, 256, 256, 4, stream);
     // Too few tiles for two blocks on a CU: two groups of waves share the steps of each.  32 rows each of
-    // 8 experts (4096 x 14336) 71 us against 81; 32 rows of 64 (2560 x 640) 26 against 21.
-    if (aligned && units < 512)
-        return launch_units(expert_tile_kernel<64, 128, 64, 32, 2, 1, 4, true>, a, 64, 128, 512, 2, stream);
+    // 8 experts (4096 x 14336) 71 us against 81, 21 rows of 21 (997 x 6104) 31 against 44; 64 rows of 30
+    // (4320 x 684) 51 against 42.
+    if (units < 512)
+        return aligned ? launch_units(expert_tile_kernel<64, 128, 64, 32, 2, 1, 4, true>, a, 64, 128, 512, 2, stream)
+                       : launch_units(expert_tile_kernel<64, 128, 64, 32, 2, 1, 4, false>, a, 64, 128, 512, 2, stream);
     return aligned ? launch_units(expert_tile_kernel<64, 128, 64, 32, 1, 1, 4, true>, a, 64, 128, 256, 2, stream)
                    : launch_units(expert_tile_kernel<64, 128, 64, 32, 1, 1, 4, false>, a, 64, 128, 256, 2, stream);
 }

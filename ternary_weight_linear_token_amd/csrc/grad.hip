@@ -182,7 +182,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     int t = blockIdx.x, slice;  // EXPERTS, MODE 0: the expert
     if constexpr (EXPERTS && MODE == 0) {
         // every XCD takes an eighth of each expert's tiles: a run of whole experts would leave the
-        // XCD with the most rows working alone (8 experts of 6912 x 2560, 4096 rows: 900 -> 320 us)
+        // XCD with the most rows working alone (8 experts of 6912 x 2560, 4096 rows: 922 -> 240 us)
         const int xcd = t & 7, b = t >> 3, share = (tiles + 7) >> 3;
         slice = __builtin_amdgcn_readfirstlane(b / share);
         t = xcd * share + (b - slice * share);
@@ -811,18 +811,26 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
 }
 
 // ---- grouped by expert ----
-// Tiles of the experts' gradients (mode, bm, bn, wm, wn, g, bl, d, w).  An expert brings few rows,
-// and with many of them there are tiles enough, so none is split and the tiles are smaller than
-// those of one large product.  dw: two blocks of 256 x 128 on a CU, one computing while the other
-// writes its outputs (8 experts of 6912 x 2560, 4096 rows, fp32: 227 us; 256 x 256 240, 128 x 128 260;
-// 16 of 641 x 2564, 258 rows: 22, 30 and 30).  dx: 64 x 256, whose rows are padded little and converted for
-// 256 columns at once (the first of these: 158 us; 64 x 128 190, 128 x 128 185, 256 x 256 190); below two
-// blocks for each CU 32 x 128 with four groups of waves (the second: 14 us against 24; 64 rows of 8 experts
-// of 6912 x 2560 34 against 92).
+// Tiles of the experts' gradients (mode, bm, bn, wm, wn, g, bl, d, w); none is split over blocks.
+// dw: 256 x 128, two blocks on a CU (512 rows each of 8 experts of 6912 x 2560, fp32: 227 us; 256 x 256
+// 240, 128 x 128 260).  128 x 128 where those leave places empty or 256 pads N by an eighth more than 128
+// (fp32, 455 rows of 6 experts of 960 x 416: 14 us against 18; bf16, 811 of 13, 789 x 2732: 117 against
+// 132; 375 of 83, 320 x 1600: 90 against 111).  128 x 128 at four blocks on a CU for few rows, where the
+// outputs are all there is to do (bf16: 5 of 42, 753 x 2680, 40 against 47; one of 75, 320 x 2432, 22
+// against 33; fp32, 65 of 6, 9093 x 1380, 49 either way).
+// dx: 64 x 256, whose rows are padded little and converted for 256 columns at once (the first of these:
+// 158 us; 64 x 128 190, 128 x 128 185, 256 x 256 190); below two blocks for each CU 32 x 128 with four
+// groups of waves (258 rows of 16, 641 x 2564: 14 us against 24; 64 of 8, 6912 x 2560: 34 against 92;
+// at 400 to 600 tiles either is up to a fifth faster); where not even those make half a block for each CU
+// 32 x 64 with eight groups, half the steps (2 rows of 3, 13666 x 1664: 64 us against 115; 10 of 10, 5311
+// x 1296: 33 against 49; with 198 tiles of 32 x 128 92 against 80).
 constexpr GradCfg kExpertCfg[] = {
     {0, 256, 128, 128, 64, 1, 32, 1, 2, 2, 0, 0, 0},
+    {0, 128, 128, 64, 64, 1, 64, 1, 2, 2, 0, 0, 0},
+    {0, 128, 128, 64, 64, 1, 32, 1, 4, 4, 0, 0, 0},
     {1, 64, 256, 64, 64, 1, 64, 1, 2, 3, 0, 0, 0},
     {1, 32, 128, 32, 64, 4, 64, 1, 2, 1, 0, 0, 0},
+    {1, 32, 64, 32, 64, 8, 64, 1, 2, 1, 0, 0, 0},
 };
 
 template <int C, Rows ROWS>
@@ -925,8 +933,10 @@ hipError_t launch_grad_input_experts(const uint16_t* const* dy, const int* offse
     a.P = (int)P;
     const int64_t active = E < P ? E : P;
     const int64_t units = active * ((P / active + 63) / 64) * ((K + 255) / 256);  // of 64 x 256, spread evenly
-    if (units >= 512) return aligned ? launch_experts<1, kWhole>(a, stream) : launch_experts<1, kOdd>(a, stream);
-    return aligned ? launch_experts<2, kWhole>(a, stream) : launch_experts<2, kOdd>(a, stream);
+    if (units >= 512) return aligned ? launch_experts<3, kWhole>(a, stream) : launch_experts<3, kOdd>(a, stream);
+    if (active * ((P / active + 31) / 32) * ((K + 127) / 128) >= kCUs / 2)  // of 32 x 128
+        return aligned ? launch_experts<4, kWhole>(a, stream) : launch_experts<4, kOdd>(a, stream);
+    return aligned ? launch_experts<5, kWhole>(a, stream) : launch_experts<5, kOdd>(a, stream);
 }
 
 hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, const float* a_scale,
@@ -945,7 +955,13 @@ hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, cons
     a.offsets = offsets;
     a.E = (int)E;
     a.P = (int)P;
-    return N % 2 == 0 ? launch_experts<0, kWhole>(a, stream) : launch_experts<0, kOddEnd>(a, stream);
+    const bool even = N % 2 == 0;
+    if (P < 64 * (E < P ? E : P) || P == 0)
+        return even ? launch_experts<2, kWhole>(a, stream) : launch_experts<2, kOddEnd>(a, stream);
+    const int64_t wide = (N + 255) / 256, narrow = (N + 127) / 128;
+    if (E * wide * ((K + 127) / 128) <= 576 || 16 * wide > 9 * narrow)
+        return even ? launch_experts<1, kWhole>(a, stream) : launch_experts<1, kOddEnd>(a, stream);
+    return even ? launch_experts<0, kWhole>(a, stream) : launch_experts<0, kOddEnd>(a, stream);
 }
 
 }  // namespace bitnet

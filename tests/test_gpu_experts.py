@@ -290,6 +290,21 @@ def test_weight_gradient(P, E, N, K, kind, dt):
     assert torch.equal(again, out)
 
 
+# sizes that reach the tiles of many rows and columns (those above are below their thresholds)
+@pytest.mark.parametrize("P,E,N,K", [(500, 4, 16400, 2064), (4200, 2, 2100, 64), (700, 70, 1100, 1024)])
+@pytest.mark.parametrize("kind", ["even", "skewed"])
+def test_large_products(P, E, N, K, kind):
+    test_product_of_sorted_rows(P, E, N, K, kind)
+
+
+@pytest.mark.parametrize("P,E,N,K", [(600, 9, 1024, 2180), (600, 9, 1023, 2176)])
+@pytest.mark.parametrize("kind", ["even", "skewed", "one"])
+def test_large_gradients(P, E, N, K, kind):
+    test_input_gradient(P, E, N, K, kind)
+    for dt in ("f32", "bf16"):
+        test_weight_gradient(P, E, N, K, kind, dt)
+
+
 def test_neighbours_stay_apart():
     # an expert's rows border on another's: values there that are not finite do not enter
     for N, K in ((33, 64), (32, 64), (641, 132)):
