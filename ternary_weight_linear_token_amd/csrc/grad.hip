@@ -815,9 +815,10 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
 // dw: 256 x 128, two blocks on a CU (512 rows each of 8 experts of 6912 x 2560, fp32: 227 us; 256 x 256
 // 240, 128 x 128 260).  128 x 128 where those leave places empty or 256 pads N by an eighth more than 128
 // (fp32, 455 rows of 6 experts of 960 x 416: 14 us against 18; bf16, 811 of 13, 789 x 2732: 117 against
-// 132; 375 of 83, 320 x 1600: 90 against 111).  128 x 128 at four blocks on a CU for few rows, where the
-// outputs are all there is to do (bf16: 5 of 42, 753 x 2680, 40 against 47; one of 75, 320 x 2432, 22
-// against 33; fp32, 65 of 6, 9093 x 1380, 49 either way).
+// 132; 375 of 83, 320 x 1600: 90 against 111).  Few rows, where the outputs are all there is to do: 128 x
+// 128 at four blocks on a CU for few tiles (fp32, 8 rows of 4, 1023 x 1020: 9 us against 11) and for bf16
+// gradients of a few million values for each expert (5 of 42, 753 x 2680: 40 against 47; one of 75, 320 x
+// 2432: 22 against 33; but 32 of 8, 6912 x 2560: 71 against 61; fp32, 16 of 16, 641 x 2564: 28 against 24).
 // dx: 64 x 256, whose rows are padded little and converted for 256 columns at once (the first of these:
 // 158 us; 64 x 128 190, 128 x 128 185, 256 x 256 190); below two blocks for each CU 32 x 128 with four
 // groups of waves (258 rows of 16, 641 x 2564: 14 us against 24; 64 of 8, 6912 x 2560: 34 against 92;
@@ -956,10 +957,11 @@ hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, cons
     a.E = (int)E;
     a.P = (int)P;
     const bool even = N % 2 == 0;
-    if (P < 64 * (E < P ? E : P) || P == 0)
+    const int64_t wide = (N + 255) / 256, narrow = (N + 127) / 128, tiles = E * wide * ((K + 127) / 128);
+    const bool few = P < 64 * (E < P ? E : P) || P == 0;
+    if (few && (tiles <= kCUs || (out_dtype == BITNET_OUT_BF16 && N * K <= (int64_t)6 << 20)))
         return even ? launch_experts<2, kWhole>(a, stream) : launch_experts<2, kOddEnd>(a, stream);
-    const int64_t wide = (N + 255) / 256, narrow = (N + 127) / 128;
-    if (E * wide * ((K + 127) / 128) <= 576 || 16 * wide > 9 * narrow)
+    if (!few && (tiles <= 576 || 16 * wide > 9 * narrow))
         return even ? launch_experts<1, kWhole>(a, stream) : launch_experts<1, kOddEnd>(a, stream);
     return even ? launch_experts<0, kWhole>(a, stream) : launch_experts<0, kOddEnd>(a, stream);
 }
