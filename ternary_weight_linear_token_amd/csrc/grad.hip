@@ -815,7 +815,9 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
 // dw: 256 x 128, two blocks on a CU (512 rows each of 8 experts of 6912 x 2560, fp32: 227 us; 256 x 256
 // 240, 128 x 128 260).  128 x 128 where those leave places empty or 256 pads N by an eighth more than 128
 // (fp32, 455 rows of 6 experts of 960 x 416: 14 us against 18; bf16, 811 of 13, 789 x 2732: 117 against
-// 132; 375 of 83, 320 x 1600: 90 against 111).  Few rows, where the outputs are all there is to do: 128 x
+// 132; 375 of 83, 320 x 1600: 90 against 111), with two groups of waves, half the steps, for many rows in
+// at most one tile for each CU (bf16, 2048 of 2, 1024 x 1024: 27 us against 34; 512 of 8, 640 x 640: 20
+// against 21; with 400 tiles 23 against 21).  Few rows, where the outputs are all there is to do: 128 x
 // 128 at four blocks on a CU for few tiles (fp32, 8 rows of 4, 1023 x 1020: 9 us against 11) and for bf16
 // gradients of a few million values for each expert (5 of 42, 753 x 2680: 40 against 47; one of 75, 320 x
 // 2432: 22 against 33; but 32 of 8, 6912 x 2560: 71 against 61; fp32, 16 of 16, 641 x 2564: 28 against 24).
@@ -829,6 +831,7 @@ constexpr GradCfg kExpertCfg[] = {
     {0, 256, 128, 128, 64, 1, 32, 1, 2, 2, 0, 0, 0},
     {0, 128, 128, 64, 64, 1, 64, 1, 2, 2, 0, 0, 0},
     {0, 128, 128, 64, 64, 1, 32, 1, 4, 4, 0, 0, 0},
+    {0, 128, 128, 64, 64, 2, 64, 1, 2, 1, 0, 0, 0},
     {1, 64, 256, 64, 64, 1, 64, 1, 2, 3, 0, 0, 0},
     {1, 32, 128, 32, 64, 4, 64, 1, 2, 1, 0, 0, 0},
     {1, 32, 64, 32, 64, 8, 64, 1, 2, 1, 0, 0, 0},
@@ -934,10 +937,10 @@ hipError_t launch_grad_input_experts(const uint16_t* const* dy, const int* offse
     a.P = (int)P;
     const int64_t active = E < P ? E : P;
     const int64_t units = active * ((P / active + 63) / 64) * ((K + 255) / 256);  // of 64 x 256, spread evenly
-    if (units >= 512) return aligned ? launch_experts<3, kWhole>(a, stream) : launch_experts<3, kOdd>(a, stream);
+    if (units >= 512) return aligned ? launch_experts<4, kWhole>(a, stream) : launch_experts<4, kOdd>(a, stream);
     if (active * ((P / active + 31) / 32) * ((K + 127) / 128) >= kCUs / 2)  // of 32 x 128
-        return aligned ? launch_experts<4, kWhole>(a, stream) : launch_experts<4, kOdd>(a, stream);
-    return aligned ? launch_experts<5, kWhole>(a, stream) : launch_experts<5, kOdd>(a, stream);
+        return aligned ? launch_experts<5, kWhole>(a, stream) : launch_experts<5, kOdd>(a, stream);
+    return aligned ? launch_experts<6, kWhole>(a, stream) : launch_experts<6, kOdd>(a, stream);
 }
 
 hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, const float* a_scale,
@@ -961,6 +964,8 @@ hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, cons
     const bool few = P < 64 * (E < P ? E : P) || P == 0;
     if (few && (tiles <= kCUs || (out_dtype == BITNET_OUT_BF16 && N * K <= (int64_t)6 << 20)))
         return even ? launch_experts<2, kWhole>(a, stream) : launch_experts<2, kOddEnd>(a, stream);
+    if (P >= 256 * (E < P ? E : P) && P > 0 && E * narrow * ((K + 127) / 128) <= kCUs)
+        return even ? launch_experts<3, kWhole>(a, stream) : launch_experts<3, kOddEnd>(a, stream);
     if (!few && (tiles <= 576 || 16 * wide > 9 * narrow))
         return even ? launch_experts<1, kWhole>(a, stream) : launch_experts<1, kOddEnd>(a, stream);
     return even ? launch_experts<0, kWhole>(a, stream) : launch_experts<0, kOddEnd>(a, stream);

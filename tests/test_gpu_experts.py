@@ -297,7 +297,7 @@ def test_large_products(P, E, N, K, kind):
     test_product_of_sorted_rows(P, E, N, K, kind)
 
 
-@pytest.mark.parametrize("P,E,N,K", [(600, 9, 1024, 2180), (600, 9, 1023, 2176)])
+@pytest.mark.parametrize("P,E,N,K", [(600, 9, 1024, 2180), (600, 9, 1023, 2176), (1100, 3, 300, 260), (1100, 3, 301, 256)])
 @pytest.mark.parametrize("kind", ["even", "skewed", "one"])
 def test_large_gradients(P, E, N, K, kind):
     test_input_gradient(P, E, N, K, kind)
