@@ -10,6 +10,7 @@ import ctypes
 import os
 import threading
 from array import array
+from operator import attrgetter
 
 import torch
 
@@ -516,11 +517,14 @@ def _scale_code(scale) -> int:
     return _SCALE_NAMES[scale] if isinstance(scale, str) else int(scale)
 
 
+_Tensor = torch.Tensor
+
+
 def _arg(t, dtype, name, shape, device):
     """Device pointer of an argument that has to lie on `device`; None (optional) stays None."""
     if t is None:
         return None
-    if type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous() and (
+    if type(t) is _Tensor and t.dtype is dtype and t.device == device and t.is_contiguous() and (
             shape is None or t.shape == shape) and not t.requires_grad:
         return t.data_ptr()
     ptr = _tensor(t, dtype, name, shape)  # raises what is wrong, or takes a subclass
@@ -872,20 +876,29 @@ def rmsnorm_backward(dy, x, weight, rstd, x_scale=None, dresidual=None, need_sum
 _GRAD_CODES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 
 
+# (map over these: a loop in Python costs twice as much for a long list)
+_dtype_of, _shape_of, _wants_grad = attrgetter("dtype"), attrgetter("shape"), attrgetter("requires_grad")
+
+
 def _grad_list(tensors, name, device):
     """Host arrays (pointers, sizes, types) of a list of fp32 and bf16 tensors on one device."""
-    index, codes = device.index, []
-    for i, t in enumerate(tensors):
-        code = _GRAD_CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-        if code is None or type(t) is not torch.Tensor or t.get_device() != index or not t.is_contiguous(
-                ) or t.requires_grad:
+    n, index = len(tensors), device.index
+    codes = None
+    if list(map(type, tensors)).count(_Tensor) == n:
+        codes = [_GRAD_CODES.get(t) for t in map(_dtype_of, tensors)]
+        if (None in codes or list(map(_Tensor.get_device, tensors)).count(index) != n or
+                not all(map(_Tensor.is_contiguous, tensors)) or any(map(_wants_grad, tensors))):
+            codes = None
+    if codes is None:  # find and raise what is wrong, or take subclasses
+        codes = []
+        for i, t in enumerate(tensors):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name}[{i}] must be a torch.Tensor")
-            if code is None:
+            if t.dtype not in _GRAD_CODES:
                 raise TypeError(f"{name}[{i}] must be torch.float32 or torch.bfloat16, got {t.dtype}")
-            _arg(t, t.dtype, f"{name}[{i}]", None, device)  # raises what is wrong, or takes a subclass
-        codes.append(code)
-    return (array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]),
+            _arg(t, t.dtype, f"{name}[{i}]", None, device)
+            codes.append(_GRAD_CODES[t.dtype])
+    return (array("Q", map(_Tensor.data_ptr, tensors)), array("q", map(_Tensor.numel, tensors)),
             array("i", codes))
 
 
@@ -932,12 +945,13 @@ def clip_grads(grads, max_norm, norm=None, out=None, workspace=None):
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must have one tensor per gradient")
-        O = _grad_list(out, "out", d)[0]
-        for i, (o, g) in enumerate(zip(out, grads)):
-            if o.shape != g.shape:
-                raise ValueError(f"out[{i}] has shape {tuple(o.shape)}, expected {tuple(g.shape)}")
-            if o.dtype is not g.dtype:
-                raise TypeError(f"out[{i}] must be {g.dtype}, got {o.dtype}")
+        O, _, types = _grad_list(out, "out", d)
+        if types != T or list(map(_shape_of, out)) != list(map(_shape_of, grads)):
+            for i, (o, g) in enumerate(zip(out, grads)):
+                if o.shape != g.shape:
+                    raise ValueError(f"out[{i}] has shape {tuple(o.shape)}, expected {tuple(g.shape)}")
+                if o.dtype is not g.dtype:
+                    raise TypeError(f"out[{i}] must be {g.dtype}, got {o.dtype}")
     ws_ptr, ws_bytes, ws = None, 0, None
     norm_in = _arg(norm, torch.float32, "norm", (), d)
     if norm is None:
@@ -965,9 +979,8 @@ def expert_order(ids, n_experts, workspace=None):
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
     E = int(n_experts)
-    rows = torch.empty((T * J,), dtype=torch.int32, device=d)
-    offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=d)
-    slots = torch.empty((T, J), dtype=torch.int32, device=d)
+    slots = torch.empty_like(ids, dtype=torch.int32, memory_format=torch.contiguous_format)
+    rows, offsets = slots.new_empty(T * J), slots.new_empty(max(E, 0) + 1)
     need = int(lib().bitnet_expert_order_workspace_size(T * J, E)) if workspace is None else 0
     ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
     _run("bitnet_expert_order", d, _arg(ids, ids.dtype, "ids", (T, J), d),
@@ -1087,7 +1100,7 @@ def combine_experts(y, slots, weights=None, out=None):
     T, J = _rows(slots, "slots")
     d = y.device
     if out is None:
-        out = torch.empty((T, D), dtype=torch.bfloat16, device=d)
+        out = y.new_empty((T, D), dtype=torch.bfloat16)
     _run("bitnet_combine_experts", d, _arg(y, torch.bfloat16, "y", (P, D), d),
          _arg(slots, torch.int32, "slots", (T, J), d),
          _arg(weights, torch.float32, "weights", (T, J), d), T, J, P, D,

@@ -290,6 +290,16 @@ def test_weight_gradient(P, E, N, K, kind, dt):
     assert torch.equal(again, out)
 
 
+def test_input_gradient_of_no_columns():
+    # products without outputs have a zero gradient, in either tile, and rows of no expert stay
+    for P, K in ((7, 64), (7, 20), (5000, 4096)):
+        off = offsets_of([P, 0])
+        none = (torch.empty((2, 0, K // 4), dtype=torch.uint8, device="cuda"), torch.empty((2, 0), device="cuda"))
+        out = torch.full((P + 2, K), 5.0, dtype=torch.bfloat16, device="cuda")
+        bw.grad_input_experts(torch.empty((P + 2, 0), dtype=torch.bfloat16, device="cuda"), off, *none, out=out)
+        assert not out[:P].any() and (out[P:] == 5.0).all()
+
+
 # sizes that reach the tiles of many rows and columns (those above are below their thresholds)
 @pytest.mark.parametrize("P,E,N,K", [(500, 4, 16400, 2064), (4200, 2, 2100, 64), (700, 70, 1100, 1024)])
 @pytest.mark.parametrize("kind", ["even", "skewed"])
