@@ -615,10 +615,11 @@ hipError_t launch_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T
     const int64_t units = active * ((per + 63) / 64) * cols;  // of 64 x 128
     const bool aligned = K % 16 == 0;
     // Few rows: the stream re-reads the activations for every 64 weight rows, 64 x 128 tiles keep
-    // them in LDS but need two blocks on a CU to hide their steps' latency.  Four rows each of 64 experts
-    // (640 x 2560, twice) 15.2 us against 19.5, 16 rows 29.3 against 24.9; four rows each of 8 experts
-    // (4096 x 14336: 256 tiles of 112 steps) 31 against 62.
-    if (aligned && (per <= 4 || (per <= 16 && units < 512))) {
+    // them in LDS but need two blocks on a CU to hide their steps' latency.  Two rows each of 64 experts
+    // (640 x 2560, twice) 13.0 us against 16.9, eight 21.2 against 21.5, 16 29.0 against 22.4; four rows
+    // each of 8 experts (4096 x 14336) 33 against 44, 16 49 against 44; with few tiles 16 rows of 4
+    // (1408 x 8192, 44 tiles) 14.4 against 21.7, of 16 (768 x 2048, 96) 9.2 against 9.3.
+    if (aligned && (per <= 8 || (per <= 16 && units <= 192))) {
         const int64_t tn = column_tiles(a, 64), tm = expert_tiles(P, E, 16);  // at most 2048 row tiles
         if (tn * tm > max_blocks(64 * kStreamWaves)) return hipErrorInvalidValue;
         hipLaunchKernelGGL(expert_stream_kernel, dim3((unsigned)tn, (unsigned)tm), dim3(64 * kStreamWaves), 0,
