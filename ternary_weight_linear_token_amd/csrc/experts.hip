@@ -387,20 +387,24 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
         }
     };
     if constexpr (G == 1) {
+        // the columns of a row one behind another, so that their stores meet in a cache line (512 rows each
+        // of 8 experts, 14336 x 4096, twice: 230 MB written instead of 407, 492 -> 470 us)
+        float sc[NB][2][8];
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float sc[8];
-                scales(i, h, sc);
+            for (int h = 0; h < 2; ++h) scales(i, h, sc[i][h]);
 #pragma unroll
-                for (int j = 0; j < MB; ++j) {
+        for (int j = 0; j < MB; ++j)
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     int v[8];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) v[r] = acc[j][i][8 * h + r];
-                    emit(j, i, h, v, sc);
+                    emit(j, i, h, v, sc[i][h]);
                 }
-            }
     } else {
         // every group leaves its sums in LDS and adds up, over the groups, the part it writes
         constexpr int EV = MB * NB * 2;  // eighths of 16 registers
@@ -627,7 +631,7 @@ hipError_t launch_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T
         return hipGetLastError();
     }
     // 128 x 256 where there are a hundred rows, one tile for every CU, and 32 steps or a thousand rows: 512
-    // rows each of 8 experts (14336 x 4096, twice) 491 us against 631 in 64 x 128 tiles and 559 in 256 x 256 ones, of
+    // rows each of 8 experts (14336 x 4096, twice) 470 us against 631 in 64 x 128 tiles and 559 in 256 x 256 ones, of
     // which a quarter is padding and one block fills a CU; 256 rows (4096 x 14336) 167 against 182.  Fewer
     // tiles: 434 rows of 3 experts (342 x 2432, twice) 38 against 14; fewer steps: 128 rows of 64
     // (2560 x 640) 44 against 37, but 4096 rows of 4 (4096 x 1280) 115 against 135; columns off 16 (rows of 4-byte loads): 884 rows of 8 (2490 x 3592)
