@@ -540,8 +540,8 @@ int bitnet_rmsnorm(const uint16_t* x, const uint16_t* residual, const float* wei
  *                the checkpoint: int8 (M, K) codes with their float (M) scales.
  *   dresidual  : bf16 (M, K), optional: the gradient that reaches the sum along the residual stream.
  *   weight     : float (K), optional (1).   rstd : of the forward.
- *   workspace  : with dweight, bitnet_rmsnorm_backward_workspace_size(M, K) bytes of scratch (else
- *                BITNET_ERR_WORKSPACE); calls that share one must be ordered.
+ *   workspace  : with dweight, bitnet_rmsnorm_backward_workspace_size(M, K) bytes of scratch (0 for
+ *                few rows; else BITNET_ERR_WORKSPACE); calls that share one must be ordered.
  */
 size_t bitnet_rmsnorm_backward_workspace_size(int64_t M, int64_t K);
 int bitnet_rmsnorm_backward(const uint16_t* dy, const void* x, const float* x_scale,

@@ -49,12 +49,13 @@ def test_rmsnorm_validation(L):
 
 
 def test_rmsnorm_backward_validation(L):
-    ws = L.bitnet_rmsnorm_backward_workspace_size(8, 256)
+    ws = L.bitnet_rmsnorm_backward_workspace_size(800, 256)
     assert ws > 0 and ws % 1024 == 0  # whole rows of fp32 partials
+    assert L.bitnet_rmsnorm_backward_workspace_size(8, 256) == 0  # a single block
     assert L.bitnet_rmsnorm_backward_workspace_size(8, 255) == 0
     assert L.bitnet_rmsnorm_backward_workspace_size(0, 256) == 0
 
-    def f(dy=A, x=B, xs=None, w=C, rstd=D, dres=E, M=8, K=256, dx=F, dw=G, ws_ptr=H, n=ws):
+    def f(dy=A, x=B, xs=None, w=C, rstd=D, dres=E, M=800, K=256, dx=F, dw=G, ws_ptr=H, n=ws):
         return L.bitnet_rmsnorm_backward(dy, x, xs, w, rstd, dres, M, K, dx, dw, ws_ptr, n, None)
     for name in ("dy", "x", "rstd", "dx"):
         assert f(**{name: None}) == INVALID, name

@@ -152,6 +152,15 @@ def test_backward(M, K, ckpt, res):
         check_back(dy, x, x, w, rstd, None, dres, f"{M}x{K}")
 
 
+@pytest.mark.parametrize("K", [256, 508, 2560, 4100, 8192, 20000])
+def test_one_block_and_several(K):
+    # column sums of a single block, and of several that a second launch joins
+    for M in (2, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65):
+        dy, x = bf16(M, K, seed=M, scale=1e-3, hot=False), bf16(M, K, seed=K)
+        _, rstd = bw.rmsnorm(x, return_stats=True)
+        check_back(dy, x, x, None, rstd, None, None, f"{M}x{K}")
+
+
 def test_backward_is_the_gradient():
     # against automatic differentiation of the definition, and against differences
     M, K = 3, 24
@@ -334,9 +343,10 @@ def test_refusals():
         bw.rmsnorm(x[:, ::2])
     with pytest.raises(bw.BitnetError):
         bw.rmsnorm(x, eps=0.0)
+    many, few = bf16(400, 256, seed=2), torch.empty(16, dtype=torch.uint8, device="cuda")
     with pytest.raises(bw.BitnetError):
-        bw.rmsnorm_backward(x, x, w, torch.ones(4, device="cuda"),
-                            workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        bw.rmsnorm_backward(many, many, w, torch.ones(400, device="cuda"), workspace=few)
+    bw.rmsnorm_backward(x, x, w, torch.ones(4, device="cuda"), workspace=few)  # a single block needs none
     with pytest.raises(ValueError):
         bw.rmsnorm(x, torch.ones(256, device="cuda", requires_grad=True))
     g = torch.ones(64, device="cuda")
