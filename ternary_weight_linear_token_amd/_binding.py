@@ -133,6 +133,8 @@ def _check(status: int, what: str):
 
 
 def _out_code(out_dtype) -> int:
+    if out_dtype in _OUT_NAMES:
+        return _OUT_NAMES[out_dtype]
     if isinstance(out_dtype, int):
         return out_dtype
     if isinstance(out_dtype, torch.dtype):
@@ -998,16 +1000,25 @@ def _experts_shape(packed, name):
 
 
 def _experts_weights(packed, w_scale, d):
-    """(E, K, row counts, host arrays) of up to MAX_GROUPS weight stacks over the same input."""
+    """(E, K, row counts, pointers, pointers) of weight stacks over the same input."""
     G = len(packed)
     if G == 0 or len(w_scale) != G:
         raise ValueError("packed and w_scale must have the same length, at least 1")
-    E, _, K = _experts_shape(packed[0], "packed[0]")
-    Ns = [_experts_shape(t, f"packed[{g}]")[1] for g, t in enumerate(packed)]
-    ptrs, sizes = _ARRAYS[G - 1] if G <= MAX_GROUPS else (ctypes.c_void_p * G, ctypes.c_int64 * G)
-    P = ptrs(*[_arg(t, torch.uint8, "packed", (E, n, K // 4), d) for t, n in zip(packed, Ns)])
-    S = ptrs(*[_arg(t, torch.float32, "w_scale", (E, n), d) for t, n in zip(w_scale, Ns)])
-    return E, K, Ns, ptrs, P, S, sizes(*Ns)
+    E, first, K = _experts_shape(packed[0], "packed[0]")
+    Ns, W, S = [], [], []
+    for g, (t, s) in enumerate(zip(packed, w_scale)):
+        n = _experts_shape(t, f"packed[{g}]")[1] if g else first
+        Ns.append(n)
+        W.append(_arg(t, torch.uint8, "packed", (E, n, K // 4), d))
+        S.append(_arg(s, torch.float32, "w_scale", (E, n), d))
+    return E, K, Ns, W, S
+
+
+def _tables(*lists):
+    """One host array of lists of equal length, and the address of each list in it."""
+    table = array("Q", [v for one in lists for v in one])
+    base, size = table.buffer_info()[0], 8 * len(lists[0])
+    return table, [base + k * size for k in range(len(lists))]
 
 
 def gemm_experts_grouped(xq, a_scale, offsets, packed, w_scale, out_dtype="f32", rows=None, out=None):
@@ -1020,19 +1031,25 @@ def gemm_experts_grouped(xq, a_scale, offsets, packed, w_scale, out_dtype="f32",
     written."""
     T, K = _rows(xq, "xq")
     d = xq.device
-    E, Kw, Ns, ptrs, W, S, NN = _experts_weights(packed, w_scale, d)
+    E, Kw, Ns, W, S = _experts_weights(packed, w_scale, d)
     if Kw != K:
         raise ValueError(f"packed has {Kw} columns, xq {K}")
     P = T if rows is None else rows.numel()
     code = _out_code(out_dtype)
-    outs = list(out) if out is not None else [None] * len(Ns)
-    if len(outs) != len(Ns):
-        raise ValueError("out must have one tensor per group")
-    outs = [_alloc_out(o, P, n, code, d) for o, n in zip(outs, Ns)]
-    O = ptrs(*[_arg(o, _OUT_TORCH[code], "out", (P, n), d) for o, n in zip(outs, Ns)])
+    dt = _OUT_TORCH[code]
+    if out is None:
+        outs = [xq.new_empty((P, n), dtype=dt) for n in Ns]
+        O = [o.data_ptr() for o in outs]
+    else:
+        outs = list(out)
+        if len(outs) != len(Ns):
+            raise ValueError("out must have one tensor per group")
+        outs = [_alloc_out(o, P, n, code, d) for o, n in zip(outs, Ns)]
+        O = [_arg(o, dt, "out", (P, n), d) for o, n in zip(outs, Ns)]
+    table, at = _tables(W, S, Ns, O)
     _run("bitnet_gemm_experts", d, _arg(xq, torch.int8, "xq", (T, K), d),
          _arg(a_scale, torch.float32, "a_scale", (T,), d), T, _arg(rows, torch.int32, "rows", (P,), d),
-         _arg(offsets, torch.int32, "offsets", (E + 1,), d), P, E, K, len(Ns), W, S, NN, O, code)
+         _arg(offsets, torch.int32, "offsets", (E + 1,), d), P, E, K, len(Ns), *at, code)
     return outs
 
 
@@ -1051,12 +1068,16 @@ def grad_input_experts_grouped(dy, offsets, packed, w_scale, out=None):
         raise ValueError("dy, packed and w_scale must have the same length, at least 1")
     P = _rows(dy[0], "dy[0]")[0]
     d = dy[0].device
-    E, K, Ns, ptrs, W, S, NN = _experts_weights(packed, w_scale, d)
+    E, K, Ns, W, S = _experts_weights(packed, w_scale, d)
     if out is None:
-        out = torch.empty((P, K), dtype=torch.bfloat16, device=d)
-    DY = ptrs(*[_arg(t, torch.bfloat16, "dy", (P, n), d) for t, n in zip(dy, Ns)])
+        out = dy[0].new_empty((P, K), dtype=torch.bfloat16)
+        dx = out.data_ptr()
+    else:
+        dx = _arg(out, torch.bfloat16, "out", (P, K), d)
+    DY = [_arg(t, torch.bfloat16, "dy", (P, n), d) for t, n in zip(dy, Ns)]
+    table, at = _tables(DY, W, S, Ns)
     _run("bitnet_grad_input_experts", d, _arg(offsets, torch.int32, "offsets", (E + 1,), d), P, E, K,
-         len(Ns), DY, W, S, NN, _arg(out, torch.bfloat16, "out", (P, K), d))
+         len(Ns), *at, dx)
     return out
 
 
@@ -1081,7 +1102,7 @@ def grad_weight_experts(dy, xq, a_scale, offsets, out_dtype="f32", rows=None, ou
         raise ValueError("offsets must be a (E + 1,) tensor")
     E = offsets.numel() - 1
     if out is None:
-        out = torch.empty((E, N, K), dtype=_OUT_TORCH[code], device=d)
+        out = dy.new_empty((E, N, K), dtype=_OUT_TORCH[code])
     need = (int(lib().bitnet_grad_weight_experts_workspace_size(P, K))
             if workspace is None and rows is not None else 0)
     ws_ptr, ws_bytes, ws = _scratch(need, workspace, d)
