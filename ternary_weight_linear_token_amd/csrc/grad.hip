@@ -826,20 +826,27 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
 // 128 at four blocks on a CU for few tiles (fp32, 8 rows of 4, 1023 x 1020: 9 us against 11) and for bf16
 // gradients of a few million values for each expert (5 of 42, 753 x 2680: 40 against 47; one of 75, 320 x
 // 2432: 22 against 33; but 32 of 8, 6912 x 2560: 71 against 61; fp32, 16 of 16, 641 x 2564: 28 against 24).
-// dx: 64 x 256, whose rows are padded little and converted for 256 columns at once (the first of these:
-// 158 us; 64 x 128 190, 128 x 128 185, 256 x 256 190); below two blocks for each CU 32 x 128 with four
-// groups of waves (258 rows of 16, 641 x 2564: 14 us against 24; 64 of 8, 6912 x 2560: 34 against 92;
-// at 400 to 600 tiles either is up to a fifth faster); where not even those make half a block for each CU
-// 32 x 64 with eight groups, half the steps (2 rows of 3, 13666 x 1664: 64 us against 115; 10 of 10, 5311
-// x 1296: 33 against 49; with 198 tiles of 32 x 128 92 against 80).
+// dx, by the number of 32 x 128 tiles: from 800 on 64 x 256, whose rows are padded little and converted
+// for 256 columns at once (512 rows of 8, 6912 x 2560: 158 us; 64 x 128 190, 128 x 128 185, 256 x 256 190;
+// with 840 tiles 19 against 27, with 504 67 against 53).  Rows off 16 bytes take two loads a chunk, which
+// want two steps in flight; two blocks share a CU then, not three, so that is for tiles that fill
+// one round of two or two of them (258 rows of 4, 5471 x 6316, 500 tiles of 64 x 256: 135 us against 186;
+// 191 of 8, 895 x 11672, 828: 52 against 67; but 539 of 4, 3319 x 3652, 540: 152 against 119).  Below 800
+// tiles 32 x 128 with four groups of waves (258 rows of 16, 641 x 2564: 14 us against 24; 64 of 8, 6912 x
+// 2560: 46 against 72), at no more than one for each CU with two steps in flight, for which there are
+// registers then (58 rows of 6, 4653 x 1176: 36 us against 45; of one step 512 x 1176 and below the same;
+// with 266 tiles 16 against 12).  Long sums in half as many: 32 x 64 with eight groups, half the steps (2
+// rows of 3, 13666 x 1664: 53 us against 87; 10 of 10, 5311 x 1296: 29 against 39; with 150 31 against 22).
 constexpr GradCfg kExpertCfg[] = {
     {0, 256, 128, 128, 64, 1, 32, 1, 2, 2, 0, 0, 0},
     {0, 128, 128, 64, 64, 1, 64, 1, 2, 2, 0, 0, 0},
     {0, 128, 128, 64, 64, 1, 32, 1, 4, 4, 0, 0, 0},
     {0, 128, 128, 64, 64, 2, 64, 1, 2, 1, 0, 0, 0},
     {1, 64, 256, 64, 64, 1, 64, 1, 2, 3, 0, 0, 0},
-    {1, 32, 128, 32, 64, 4, 64, 1, 2, 1, 0, 0, 0},
-    {1, 32, 64, 32, 64, 8, 64, 1, 2, 1, 0, 0, 0},
+    {1, 64, 256, 64, 64, 1, 64, 2, 2, 2, 0, 0, 0},
+    {1, 32, 128, 32, 64, 4, 64, 1, 2, 2, 0, 0, 0},
+    {1, 32, 128, 32, 64, 4, 64, 2, 2, 1, 0, 0, 0},
+    {1, 32, 64, 32, 64, 8, 64, 2, 2, 1, 0, 0, 0},
 };
 
 template <int C, Rows ROWS>
@@ -940,11 +947,20 @@ hipError_t launch_grad_input_experts(const uint16_t* const* dy, const int* offse
     a.offsets = offsets;
     a.E = (int)E;
     a.P = (int)P;
+    // tiles of 32 x 128 if the rows are spread evenly, and of 64 x 256 with half a tile of padding each
     const int64_t active = E < P ? E : P;
-    const int64_t units = active * ((P / active + 63) / 64) * ((K + 255) / 256);  // of 64 x 256, spread evenly
-    if (units >= 512) return aligned ? launch_experts<4, kWhole>(a, stream) : launch_experts<4, kOdd>(a, stream);
-    if (active * ((P / active + 31) / 32) * ((K + 127) / 128) >= kCUs / 2)  // of 32 x 128
-        return aligned ? launch_experts<5, kWhole>(a, stream) : launch_experts<5, kOdd>(a, stream);
+    const int64_t small = active * ((P / active + 31) / 32) * ((K + 127) / 128);
+    const int64_t rows64 = (P + 32 * active) / 64, large = (rows64 > active ? rows64 : active) * ((K + 255) / 256);
+    int64_t sum = 0;
+    for (int q = 0; q < a.groups; ++q) sum += a.L[q];
+    if (small >= 800) {
+        if (aligned) return launch_experts<4, kWhole>(a, stream);
+        return large <= 2 * kCUs || (large > 3 * kCUs && large <= 4 * kCUs) ? launch_experts<5, kOdd>(a, stream)
+                                                                            : launch_experts<4, kOdd>(a, stream);
+    }
+    if (small <= kCUs / 2 && sum >= 1024)
+        return aligned ? launch_experts<8, kWhole>(a, stream) : launch_experts<8, kOdd>(a, stream);
+    if (small <= kCUs) return aligned ? launch_experts<7, kWhole>(a, stream) : launch_experts<7, kOdd>(a, stream);
     return aligned ? launch_experts<6, kWhole>(a, stream) : launch_experts<6, kOdd>(a, stream);
 }
 

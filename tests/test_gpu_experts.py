@@ -300,14 +300,16 @@ def test_input_gradient_of_no_columns():
         assert not out[:P].any() and (out[P:] == 5.0).all()
 
 
-# sizes that reach the tiles of many rows and columns (those above are below their thresholds)
+# sizes that reach the tiles of many rows and columns, and of long sums (those above are below their
+# thresholds)
 @pytest.mark.parametrize("P,E,N,K", [(500, 4, 16400, 2064), (4200, 2, 2100, 64), (700, 70, 1100, 1024)])
 @pytest.mark.parametrize("kind", ["even", "skewed"])
 def test_large_products(P, E, N, K, kind):
     test_product_of_sorted_rows(P, E, N, K, kind)
 
 
-@pytest.mark.parametrize("P,E,N,K", [(600, 9, 1024, 2180), (600, 9, 1023, 2176), (1100, 3, 300, 260), (1100, 3, 301, 256)])
+@pytest.mark.parametrize("P,E,N,K", [(600, 9, 1024, 2180), (600, 9, 1023, 2176), (1100, 3, 300, 260), (1100, 3, 301, 256),
+                                     (40, 3, 1100, 260), (40, 3, 1104, 272), (1500, 64, 33, 1540)])
 @pytest.mark.parametrize("kind", ["even", "skewed", "one"])
 def test_large_gradients(P, E, N, K, kind):
     test_input_gradient(P, E, N, K, kind)
