@@ -849,15 +849,15 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
 
 // ---- grouped by expert ----
 // Tiles of the experts' gradients (mode, bm, bn, wm, wn, g, bl, d, w); none is split over blocks.
-// dw: 256 x 128, two blocks on a CU (512 rows each of 8 experts of 6912 x 2560, fp32: 227 us; 256 x 256
-// 240, 128 x 128 260).  128 x 128 where those leave places empty or 256 pads N by an eighth more than 128
-// (fp32, 455 rows of 6 experts of 960 x 416: 14 us against 18; bf16, 811 of 13, 789 x 2732: 117 against
-// 132; 375 of 83, 320 x 1600: 90 against 111), with two groups of waves, half the steps, for many rows in
-// at most one tile for each CU (bf16, 2048 of 2, 1024 x 1024: 27 us against 34; 512 of 8, 640 x 640: 20
-// against 21; with 400 tiles 23 against 21).  Few rows, where the outputs are all there is to do: 128 x
-// 128 at four blocks on a CU for few tiles (fp32, 8 rows of 4, 1023 x 1020: 9 us against 11) and for bf16
-// gradients of a few million values for each expert (5 of 42, 753 x 2680: 40 against 47; one of 75, 320 x
-// 2432: 22 against 33; but 32 of 8, 6912 x 2560: 71 against 61; fp32, 16 of 16, 641 x 2564: 28 against 24).
+// dw: 128 x 128, three blocks on a CU (fp32, 216 rows of 37, 384 x 2752: 50 us; two blocks and steps of 64
+// rows 57; 3 of 44, 320 x 2992: 27 us, 256 x 128 30; bf16, 23 of 38, 6733 x 516: 99 us, four blocks 111).
+// Hundreds of rows or thousands of tiles: 256 x 128 (bf16, 1393 of 7, 2112 x 2496: 143 us against 150; 124
+// of 16, 3106 x 1476: 53 against 58), unless 256 pads N by an eighth more than 128.  Rows off a dword (N
+// odd) cost two loads a chunk and want two steps in flight: 128 x 128 with steps of 64 rows for hundreds
+// of rows, fp32 in thousands of tiles or few tiles (bf16, 729 of 9, 4021 x 1932: 233 us against 298 in 256
+// x 128; fp32, 153 of 34, 2497 x 1576: 222 against 279; but bf16, 141 of 11, 3569 x 2620: 111 against 99).
+// Many rows in at most one tile for each CU: two groups of waves, half the steps (bf16, 2048 of 2, 1024 x
+// 1024: 27 us against 34; N odd, 2228 of 6, 343 x 640: 39 with two steps in flight, 45 with one).
 // dx, by the number of 32 x 128 tiles: from 800 on 64 x 256, whose rows are padded little and converted
 // for 256 columns at once (512 rows of 8, 6912 x 2560: 158 us; 64 x 128 190, 128 x 128 185, 256 x 256 190;
 // with 840 tiles 19 against 27, with 504 67 against 53).  Rows off 16 bytes take two loads a chunk, which
@@ -871,9 +871,10 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
 // rows of 3, 13666 x 1664: 53 us against 87; 10 of 10, 5311 x 1296: 29 against 39; with 150 31 against 22).
 constexpr GradCfg kExpertCfg[] = {
     {0, 256, 128, 128, 64, 1, 32, 1, 2, 2, 0, 0, 0},
-    {0, 128, 128, 64, 64, 1, 64, 1, 2, 2, 0, 0, 0},
-    {0, 128, 128, 64, 64, 1, 32, 1, 4, 4, 0, 0, 0},
+    {0, 128, 128, 64, 64, 1, 64, 2, 2, 2, 0, 0, 0},
+    {0, 128, 128, 64, 64, 1, 32, 1, 3, 3, 0, 0, 0},
     {0, 128, 128, 64, 64, 2, 64, 1, 2, 1, 0, 0, 0},
+    {0, 128, 128, 64, 64, 2, 64, 2, 2, 1, 0, 0, 0},
     {1, 64, 256, 64, 64, 1, 64, 1, 2, 3, 0, 0, 0},
     {1, 64, 256, 64, 64, 1, 64, 2, 2, 2, 0, 0, 0},
     {1, 32, 128, 32, 64, 4, 64, 1, 2, 2, 0, 0, 0},
@@ -986,14 +987,14 @@ hipError_t launch_grad_input_experts(const uint16_t* const* dy, const int* offse
     int64_t sum = 0;
     for (int q = 0; q < a.groups; ++q) sum += a.L[q];
     if (small >= 800) {
-        if (aligned) return launch_experts<4, kWhole>(a, stream);
-        return large <= 2 * kCUs || (large > 3 * kCUs && large <= 4 * kCUs) ? launch_experts<5, kOdd>(a, stream)
-                                                                            : launch_experts<4, kOdd>(a, stream);
+        if (aligned) return launch_experts<5, kWhole>(a, stream);
+        return large <= 2 * kCUs || (large > 3 * kCUs && large <= 4 * kCUs) ? launch_experts<6, kOdd>(a, stream)
+                                                                            : launch_experts<5, kOdd>(a, stream);
     }
     if (small <= kCUs / 2 && sum >= 1024)
-        return aligned ? launch_experts<8, kWhole>(a, stream) : launch_experts<8, kOdd>(a, stream);
-    if (small <= kCUs) return aligned ? launch_experts<7, kWhole>(a, stream) : launch_experts<7, kOdd>(a, stream);
-    return aligned ? launch_experts<6, kWhole>(a, stream) : launch_experts<6, kOdd>(a, stream);
+        return aligned ? launch_experts<9, kWhole>(a, stream) : launch_experts<9, kOdd>(a, stream);
+    if (small <= kCUs) return aligned ? launch_experts<8, kWhole>(a, stream) : launch_experts<8, kOdd>(a, stream);
+    return aligned ? launch_experts<7, kWhole>(a, stream) : launch_experts<7, kOdd>(a, stream);
 }
 
 hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, const float* a_scale,
@@ -1013,15 +1014,17 @@ hipError_t launch_grad_weight_experts(const uint16_t* dy, const int8_t* xq, cons
     a.E = (int)E;
     a.P = (int)P;
     const bool even = N % 2 == 0;
-    const int64_t wide = (N + 255) / 256, narrow = (N + 127) / 128, tiles = E * wide * ((K + 127) / 128);
-    const bool few = P < 64 * (E < P ? E : P) || P == 0;
-    if (few && (tiles <= kCUs || (out_dtype == BITNET_OUT_BF16 && N * K <= (int64_t)6 << 20)))
-        return even ? launch_experts<2, kWhole>(a, stream) : launch_experts<2, kOddEnd>(a, stream);
-    if (P >= 256 * (E < P ? E : P) && P > 0 && E * narrow * ((K + 127) / 128) <= kCUs)
-        return even ? launch_experts<3, kWhole>(a, stream) : launch_experts<3, kOddEnd>(a, stream);
-    if (!few && (tiles <= 576 || 16 * wide > 9 * narrow))
-        return even ? launch_experts<1, kWhole>(a, stream) : launch_experts<1, kOddEnd>(a, stream);
-    return even ? launch_experts<0, kWhole>(a, stream) : launch_experts<0, kOddEnd>(a, stream);
+    const int64_t wide = (N + 255) / 256, narrow = (N + 127) / 128, cols = (K + 127) / 128;
+    const int64_t per = P > 0 ? P / (E < P ? E : P) : 0;
+    if (per >= 256 && E * narrow * cols <= kCUs)
+        return even ? launch_experts<3, kWhole>(a, stream) : launch_experts<4, kOddEnd>(a, stream);
+    const int64_t tiles = E * wide * cols;  // of 256 x 128
+    const bool large = per >= 64 && tiles >= 2400;
+    if (even && 16 * wide <= 9 * narrow && (large || (per >= 400 && tiles > 576)))
+        return launch_experts<0, kWhole>(a, stream);
+    if (!even && ((large && out_dtype == BITNET_OUT_F32) || per >= 360 || (per >= 192 && tiles <= kCUs)))
+        return launch_experts<1, kOddEnd>(a, stream);
+    return even ? launch_experts<2, kWhole>(a, stream) : launch_experts<2, kOddEnd>(a, stream);
 }
 
 }  // namespace bitnet

@@ -309,7 +309,8 @@ def test_large_products(P, E, N, K, kind):
 
 
 @pytest.mark.parametrize("P,E,N,K", [(600, 9, 1024, 2180), (600, 9, 1023, 2176), (1100, 3, 300, 260), (1100, 3, 301, 256),
-                                     (40, 3, 1100, 260), (40, 3, 1104, 272), (1500, 64, 33, 1540)])
+                                     (40, 3, 1100, 260), (40, 3, 1104, 272), (1500, 64, 33, 1540),
+                                     (1700, 4, 1280, 4100), (1100, 3, 1281, 1028), (1400, 20, 1023, 3856)])
 @pytest.mark.parametrize("kind", ["even", "skewed", "one"])
 def test_large_gradients(P, E, N, K, kind):
     test_input_gradient(P, E, N, K, kind)
