@@ -444,10 +444,13 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
 // ----------------------------------------------------------------------- few rows
 constexpr int kStreamWaves = 4;
 
-// 16 rows of one expert times 64 rows of its weights and all of K (K % 16 == 0).  Wave w takes the
+// 16 rows of one expert times 64 rows of its weights and all of K.  Wave w takes the
 // 256-weight chunks w, w + 4, ..; it has the weights of one chunk in flight, which come from memory,
 // and the activations of two halves of a chunk, which come from a cache: with few registers for
-// each, a CU holds the five blocks that hide both.
+// each, a CU holds the five blocks that hide both.  Rows of weights at any byte (K % 16 != 0): a weight
+// dword is put together from the aligned ones around it when it is used (4100 columns of 8 rows each of
+// another expert, 14336 twice: 42 us, in 64 x 128 tiles 73; of 4096 columns 35).
+template <bool ALIGNED>
 __global__ __launch_bounds__(64 * kStreamWaves, 5) void expert_stream_kernel(ExpertArgs p) {
     constexpr int NB = 4, BM = 16, BN = 16 * NB, TH = 64 * kStreamWaves;
     constexpr int MO = BM * BN / TH;  // outputs of a thread
@@ -463,18 +466,27 @@ __global__ __launch_bounds__(64 * kStreamWaves, 5) void expert_stream_kernel(Exp
     const int K = p.K, N = u.N, row_bytes = K / 4;
     const int nch = (K + 255) / 256;
     const int rows_b = min(BN, N - u.n0);
-    const __amdgpu_buffer_rsrc_t rb = rsrc(
-        pick(p.packed, u.g) + ((int64_t)u.e * N + u.n0) * row_bytes, (uint32_t)(rows_b * row_bytes));
-    uint32_t voff_b[NB];
+    const uint8_t* const wbase = pick(p.packed, u.g) + ((int64_t)u.e * N + u.n0) * row_bytes;
+    const uint32_t skew = ALIGNED ? 0u : (uint32_t)((uintptr_t)wbase & 3);
+    const __amdgpu_buffer_rsrc_t rb = rsrc(wbase - skew, ALIGNED ? (uint32_t)(rows_b * row_bytes)
+                                                                 : (uint32_t)((rows_b * row_bytes + skew + 3) & ~3u));
+    uint32_t voff_b[NB], shift[NB];  // of the dword that holds the first weight; bits in front of it
 #pragma unroll
-    for (int i = 0; i < NB; ++i)  // rows behind the last one read zeros
-        voff_b[i] = 16 * i + l16 < rows_b ? (uint32_t)((16 * i + l16) * row_bytes + 16 * q) : kOut;
+    for (int i = 0; i < NB; ++i) {  // rows behind the last one read zeros
+        const uint32_t off = (uint32_t)((16 * i + l16) * row_bytes + 16 * q) + skew;
+        voff_b[i] = 16 * i + l16 < rows_b ? off & ~3u : kOut;
+        shift[i] = 8 * (off & 3);
+    }
     u32x4 w[NB];
+    uint32_t w4[ALIGNED ? 1 : NB];  // the fifth dword
     auto load_w = [&](int j) {
         const int ch = wave + kStreamWaves * j;
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-            w[i] = load16(rb, ch < nch && voff_b[i] != kOut ? voff_b[i] + 64 * ch : kOut, 0);
+        for (int i = 0; i < NB; ++i) {
+            const uint32_t off = ch < nch && voff_b[i] != kOut ? voff_b[i] + 64 * ch : kOut;
+            w[i] = load16(rb, off, 0);
+            if constexpr (!ALIGNED) w4[i] = __builtin_amdgcn_raw_buffer_load_b32(rb, off + 16, 0, 0);
+        }
     };
     load_w(0);
     const __amdgpu_buffer_rsrc_t ra =
@@ -506,6 +518,13 @@ __global__ __launch_bounds__(64 * kStreamWaves, 5) void expert_stream_kernel(Exp
     for (int i = 0; i < NB; ++i) acc[i] = v4i{0, 0, 0, 0};
     const int nj = (nch - wave + kStreamWaves - 1) / kStreamWaves;
     for (int j = 0; j < nj; ++j) {
+        if (!ALIGNED && 256 * (wave + kStreamWaves * j) + 256 > K) {
+            // what lies behind the row's end
+            const int left = K - 256 * (wave + kStreamWaves * j) - 64 * q;  // bytes, a multiple of 4
+#pragma unroll
+            for (int d = 0; d < 16; ++d)
+                x[d >> 3][(d >> 2) & 1][d & 3] = left > 4 * d ? x[d >> 3][(d >> 2) & 1][d & 3] : 0u;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -516,7 +535,9 @@ __global__ __launch_bounds__(64 * kStreamWaves, 5) void expert_stream_kernel(Exp
                 const v4i a = {(int)e[0], (int)e[1], (int)e[2], (int)e[3]};
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    const uint32_t b = w[i][2 * h + s];
+                    uint32_t b = w[i][2 * h + s];
+                    if constexpr (!ALIGNED)
+                        b = __builtin_amdgcn_alignbit(2 * h + s < 3 ? w[i][(2 * h + s + 1) & 3] : w4[i], b, shift[i]);
                     const v4i c = {(int)ternary_field_i8<0>(b), (int)ternary_field_i8<1>(b),
                                    (int)ternary_field_i8<2>(b), (int)ternary_field_i8<3>(b)};
                     acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, a, acc[i], 0, 0, 0);
@@ -627,12 +648,17 @@ hipError_t launch_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T
     // them in LDS but need two blocks on a CU to hide their steps' latency.  Two rows each of 64 experts
     // (640 x 2560, twice) 13.0 us against 16.9, eight 21.2 against 21.5, 16 29.0 against 22.4; four rows
     // each of 8 experts (4096 x 14336) 33 against 44, 16 49 against 44; with few tiles 16 rows of 4
-    // (1408 x 8192, 44 tiles) 14.4 against 21.7, of 16 (768 x 2048, 96) 9.2 against 9.3.
-    if (aligned && (per <= 8 || (per <= 16 && units <= 192))) {
+    // (1408 x 8192, 44 tiles) 14.4 against 21.7, of 16 (768 x 2048, 96) 9.2 against 9.3.  Columns off 16 cost
+    // the tiles more: 16 rows of 8 (14336 x 4100) 64 against 74, but 12 of 64 (640 x 644, twice) 14.9 against 13.3.
+    if (per <= 8 || (per <= 16 && (units <= 192 || (!aligned && K >= 2048)))) {
         const int64_t tn = column_tiles(a, 64), tm = expert_tiles(P, E, 16);  // at most 2048 row tiles
         if (tn * tm > max_blocks(64 * kStreamWaves)) return hipErrorInvalidValue;
-        hipLaunchKernelGGL(expert_stream_kernel, dim3((unsigned)tn, (unsigned)tm), dim3(64 * kStreamWaves), 0,
-                           stream, a);
+        if (aligned)
+            hipLaunchKernelGGL(expert_stream_kernel<true>, dim3((unsigned)tn, (unsigned)tm), dim3(64 * kStreamWaves),
+                               0, stream, a);
+        else
+            hipLaunchKernelGGL(expert_stream_kernel<false>, dim3((unsigned)tn, (unsigned)tm),
+                               dim3(64 * kStreamWaves), 0, stream, a);
         return hipGetLastError();
     }
     // 128 x 256 where there are a hundred rows, one tile for every CU, and 32 steps or a thousand rows: 512
