@@ -21,9 +21,9 @@
 // A K that ends inside a step reads zeros of xq behind its end (whole chunks through the buffer
 // descriptor's bounds, else by a mask); the weights behind the end are whatever lies there, times
 // zero.  Rows behind an expert's last are computed from zeros and never stored.
-// Measured: one token, two of 8 experts of 14336 x 4096, gate and up 15.9 us (59 MB, 3.7 TB/s: the launch
+// Measured: one token, two of 8 experts of 14336 x 4096, gate and up 15.7 us (59 MB, 3.8 TB/s: the launch
 // and one chain of loads, products and the join of four waves); 32 tokens, 8 of 64 experts of 640 x 2560
-// 15.9 us (53 MB); 4096 rows of 8 experts of 14336 x 4096, gate and up 458 to 470 us (2.05 to 2.1 POP/s, the
+// 15.4 us (53 MB); 4096 rows of 8 experts of 14336 x 4096, gate and up 458 to 490 us (1.96 to 2.1 POP/s, the
 // matrix cores busy 61% of the cycles of a chip that holds about 1.8 GHz under such a load; a library's
 // int8 product of one large matrix 2.07).
 #include <type_traits>

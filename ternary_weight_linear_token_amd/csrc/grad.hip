@@ -55,8 +55,8 @@
 // 256 CUs, one block on each, and a chain of 30 short steps.  dw 512 x 6912 x 2560 fp32 33 to 36 us
 // against 16.3 for its 79 MB: 1080 tiles on 1024 places leave a last round of 56 (the kernel is
 // held to 128 registers for them and keeps up to six in scratch).
-// By expert, 4096 rows of 8 experts of 6912 x 2560: dx 158 to 170 us (855 to 918 TFLOP/s, the matrix
-// cores busy 44%), dw fp32 214 to 227 (566 MB of outputs alone 104, the products 124).
+// By expert, 4096 rows of 8 experts of 6912 x 2560: dx 159 to 165 us (880 to 912 TFLOP/s, the matrix
+// cores busy 46%), dw fp32 214 to 227 (566 MB of outputs alone 104, the products 124).
 #include <cmath>
 #include <type_traits>
 #include <utility>
