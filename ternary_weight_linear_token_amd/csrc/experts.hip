@@ -650,9 +650,9 @@ hipError_t launch_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T
     // each of 8 experts (4096 x 14336) 33 against 44, 16 49 against 44; with few tiles 16 rows of 4
     // (1408 x 8192, 44 tiles) 14.4 against 21.7, of 16 (768 x 2048, 96) 9.2 against 9.3.  Columns off 16 cost
     // the tiles more: 16 rows of 8 (14336 x 4100) 64 against 74, but 12 of 64 (640 x 644, twice) 14.9 against 13.3.
-    if (per <= 8 || (per <= 16 && (units <= 192 || (!aligned && K >= 2048)))) {
-        const int64_t tn = column_tiles(a, 64), tm = expert_tiles(P, E, 16);  // at most 2048 row tiles
-        if (tn * tm > max_blocks(64 * kStreamWaves)) return hipErrorInvalidValue;
+    const bool few = per <= 8 || (per <= 16 && (units <= 192 || (!aligned && K >= 2048)));
+    const int64_t tn = few ? column_tiles(a, 64) : 0, tm = few ? expert_tiles(P, E, 16) : 0;  // at most 2048 row tiles
+    if (few && tn * tm <= max_blocks(64 * kStreamWaves)) {  // (the tiles are launched in parts)
         if (aligned)
             hipLaunchKernelGGL(expert_stream_kernel<true>, dim3((unsigned)tn, (unsigned)tm), dim3(64 * kStreamWaves),
                                0, stream, a);

@@ -217,6 +217,20 @@ def test_outputs_past_32_bits():
     assert not dx[:-5].any()
 
 
+def test_more_tiles_than_a_launch():
+    # 1472 row tiles of 16 times 16384 column tiles of 64 are more blocks than one launch takes
+    E, N, K, c = 1024, 1 << 20, 4, 8
+    packed = torch.randint(0, 3, (E, N, 4), device="cuda", dtype=torch.uint8)
+    packed = (packed[..., 0] | packed[..., 1] << 2 | packed[..., 2] << 4 | packed[..., 3] << 6)[..., None].contiguous()
+    s = torch.rand((E, N), device="cuda") + 0.5
+    xq, a = bw.quant_act(bf16(E * c, K, seed=1))
+    out = bw.gemm_experts(xq, a, offsets_of([c] * E), packed, s, "bf16")
+    for e in (0, 511, 1023):
+        r = slice(e * c, (e + 1) * c)
+        ref = xq[r].double() @ weights64(packed[e].clone(), s[e], K).t().contiguous() / a[r].double()[:, None]
+        close(out[r], ref, (BF + 3.1 * U) * ref.abs(), f"expert {e}")
+
+
 # --------------------------------------------------------------------------- gradients
 
 GRADS = [(1, 2, 1, 4), (3, 2, 17, 20), (5, 3, 640, 2560), (40, 4, 63, 252), (100, 16, 641, 2564), (300, 3, 257, 1028),
