@@ -12,9 +12,10 @@
 
 namespace bitnet {
 
-// Most tiles of `bm` rows that P rows of E experts can make.
-inline int64_t expert_tiles(int64_t P, int64_t E, int bm) {
-    const int64_t e = E < P ? E : P;
+// Most tiles of `bm` rows that P rows of E experts can make (P up to 2^30, so 31 bits hold the sum).
+template <class T>
+__host__ __device__ __forceinline__ T expert_tiles(T P, T E, int bm) {
+    const T e = E < P ? E : P;
     return (P + e * (bm - 1)) / bm;
 }
 
@@ -33,9 +34,29 @@ __device__ __forceinline__ int wave_scan(int v) {
 struct ExpertRows {
     int first, count;
 };
-__device__ __forceinline__ ExpertRows expert_rows(const int* offsets, int e, int P) {
-    const int a = min(max(offsets[e], 0), P), b = min(max(offsets[e + 1], 0), P);
+__host__ __device__ __forceinline__ ExpertRows expert_rows(const int* offsets, int e, int P) {
+    auto inside = [P](int v) { return v < 0 ? 0 : (v < P ? v : P); };
+    const int a = inside(offsets[e]), b = inside(offsets[e + 1]);
     return {a, b > a ? b - a : 0};
+}
+
+// Tiles of BM rows of the experts per * lane .. of one lane; `last`: the rows of the last of them.
+// Offsets that go up and down may give every second expert all P rows.  The bound, which sorted rows
+// do not pass, keeps the sum over the 64 lanes within 31 bits even then (tiles of fewer than 64 rows are
+// taken for few rows only).
+template <int BM>
+__host__ __device__ __forceinline__ int lane_tiles(const int* offsets, int E, int P, int per, int lane,
+                                                   ExpertRows& last) {
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = lane * per + i;
+        if (e < E) {
+            last = expert_rows(offsets, e, P);
+            sum += (last.count + BM - 1) / BM;
+        }
+    }
+    const int bound = P / BM + per;
+    return sum < bound ? sum : bound;
 }
 
 // The tiles of BM rows of all experts, in the experts' order.
@@ -49,17 +70,11 @@ struct ExpertTiles {
     __device__ __forceinline__ ExpertTiles(const int* off, int experts, int rows)
         : offsets(off), E(experts), P(rows), per((experts + 63) >> 6), sum(0), mine{0, 0} {
         const int lane = threadIdx.x & 63;
-        if (per == 1) {
-            if (lane < E) mine = expert_rows(offsets, lane, P);
-            sum = (mine.count + BM - 1) / BM;
-        } else {
-            for (int i = 0; i < per; ++i) {
-                const int e = lane * per + i;
-                if (e < E) sum += (expert_rows(offsets, e, P).count + BM - 1) / BM;
-            }
-        }
+        sum = per == 1 ? lane_tiles<BM>(offsets, E, P, 1, lane, mine)
+                       : lane_tiles<BM>(offsets, E, P, per, lane, mine);
         scan = wave_scan(sum);
-        total = __builtin_amdgcn_readlane(scan, 63);
+        // no more than the host counted on
+        total = min(__builtin_amdgcn_readlane(scan, 63), expert_tiles(P, E, BM));
     }
 
     // Expert, first row and number of rows (at most BM) of tile t < total; all uniform.
