@@ -103,6 +103,7 @@ struct GradArgs {
     // b, scale (MODE 1) and out (MODE 0) hold one matrix per expert.  MODE 1: I is P; MODE 0: L[0].
     const int* offsets;
     int E, P;
+    int first;  // first block of this launch
 };
 
 struct NoTiles {
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void grad_kernel
     std::conditional_t<EXPERTS && MODE == 1, ExpertTiles<BM>, NoTiles> rows_of(p.offsets, p.E, p.P);
     if constexpr (EXPERTS && MODE == 1) tiles_i = rows_of.total;
     const int tiles = tiles_i * p.tiles_j;
-    int t = blockIdx.x, slice;  // EXPERTS, MODE 0: the expert
+    int t = (EXPERTS ? p.first : 0) + (int)blockIdx.x, slice;  // EXPERTS, MODE 0: slice is the expert
     if constexpr (EXPERTS && MODE == 0) {
         // every XCD takes an eighth of each expert's tiles: a run of whole experts would leave the
         // XCD with the most rows working alone (8 experts of 6912 x 2560, 4096 rows: 922 -> 240 us)
@@ -890,13 +891,19 @@ hipError_t launch_experts(GradArgs a, hipStream_t stream) {
     const int64_t tj = (a.J + k.bn - 1) / k.bn;
     // MODE 0: the tiles of an expert in eighths, one for each XCD
     const int64_t blocks = (ti * tj + 7) / 8 * 8 * (k.mode == 0 ? a.E : 1);
-    if (blocks > max_blocks(threads)) return hipErrorInvalidValue;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;  // (more outputs than the card holds)
     a.tiles_i = (int)ti;
     a.tiles_j = (int)tj;
     for (int q = 0; q < a.groups; ++q) a.steps += (a.L[q] + k.bl - 1) / k.bl;  // MODE 1
-    hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, ROWS, true>),
-                       dim3((unsigned)blocks), dim3(threads), 0, stream, a);
-    return hipGetLastError();
+    constexpr int64_t most = max_blocks(threads) / 8 * 8;  // of a launch
+    for (int64_t b = 0; b < blocks; b += most) {
+        a.first = (int)b;
+        hipLaunchKernelGGL((grad_kernel<k.mode, k.bm, k.bn, k.wm, k.wn, k.g, k.bl, k.d, k.w, ROWS, true>),
+                           dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(threads), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

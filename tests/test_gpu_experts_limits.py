@@ -4,6 +4,7 @@ import torch
 
 import ternary_weight_linear_token_amd as bw
 from test_gpu_experts import experts, offsets_of
+from test_gpu_train import bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +25,43 @@ def test_offsets_that_make_no_sense_of_many_rows():
     dx = bw.grad_input_experts(out, off, packed, s)
     torch.cuda.synchronize()
     assert out.shape == (P, N) and dx.shape == (P, K)
+
+
+def test_input_gradient_of_more_tiles_than_a_launch():
+    # 2^30 rows, the most there may be, are 2^24 tiles of 64; with one output column of an expert dx is
+    # bf16(dy s) times a ternary weight, exactly
+    P, E, N, K = 1 << 30, 3, 1, 4
+    packed, s = experts(E, N, K, seed=1)
+    s = torch.tensor([[0.75], [1.5], [0.3]], device="cuda")
+    counts = [5, (1 << 29) + 77, (1 << 29) - 82]
+    table = bf16(4093, N, seed=2)
+    dy = table.repeat(P // 4093 + 1, 1)[:P]
+    dx = bw.grad_input_experts(dy, offsets_of(counts), packed, s)
+    at = 0
+    for e, c in enumerate(counts):
+        w = bw.unpack_weights(packed[e].clone(), K).to(torch.bfloat16)
+        scaled = (table.float() * s[e]).to(torch.bfloat16) * w
+        for lo in range(at, at + c, 4093 << 12):
+            n = min(4093 << 12, at + c - lo)
+            want = scaled.roll(-(lo % 4093), 0).repeat(n // 4093 + 1, 1)[:n]
+            assert (dx[lo:lo + n] == want).all(), (e, lo)
+        at += c
+
+
+def test_product_of_more_tiles_than_a_launch():
+    # four stacks of one column and 2^28 + 2^22 rows: 4.3 million row tiles times four column tiles
+    P, E, K = (1 << 28) + (1 << 22), 3, 4
+    w = [experts(E, 1, K, seed=i) for i in range(4)]
+    counts = [7, 1 << 28, (1 << 22) - 7]
+    table = codes_of(4093, K, seed=1)
+    xq = table.repeat(P // 4093 + 1, 1)[:P]
+    outs = bw.gemm_experts_grouped(xq, torch.ones(P, device="cuda"), offsets_of(counts), [p for p, _ in w],
+                                   [s for _, s in w], "i32")
+    for g, (packed, _) in enumerate(w):
+        at = 0
+        for e, c in enumerate(counts):
+            want = (table.float() @ bw.unpack_weights(packed[e].clone(), K).float().t().contiguous()).int()
+            for lo in range(at, at + c, 4093 << 12):
+                n = min(4093 << 12, at + c - lo)
+                assert torch.equal(outs[g][lo:lo + n], want.roll(-(lo % 4093), 0).repeat(n // 4093 + 1, 1)[:n])
+            at += c
