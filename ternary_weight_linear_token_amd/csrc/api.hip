@@ -9,7 +9,6 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <new>
 
 #include "bitnet_w2a8.h"
 #include "kernels.hpp"
@@ -731,37 +730,53 @@ int bitnet_grad_norm(int64_t count, const void* const* grads, const int64_t* n, 
 }
 
 // Whether an output overlaps another output, or an input that is not its own (out[i] == grads[i]
-// exactly).  Spans sorted by their start: an output may not begin before the furthest end of the
-// spans in front of it, nor an input before that of the outputs.
+// exactly).  In the order of their starts an output may not begin before the furthest end of the spans in
+// front of it, nor an input before that of the outputs.  The spans pass in that order through a buffer on
+// the stack: all that fit, or the lowest half buffer of those not seen yet, so that longer lists are read
+// again for each.
 static int check_clip_outputs(int64_t count, const void* const* grads, void* const* out, const int64_t* n,
                               const int32_t* dtype) {
     struct Span {
-        uintptr_t begin, end;
-        bool out;
+        uintptr_t begin;
+        int64_t i;  // even: output, odd: input of tensor i / 2
+        bool operator<(const Span& b) const { return begin != b.begin ? begin < b.begin : i < b.i; }
     };
-    Span* const spans = new (std::nothrow) Span[2 * (size_t)count + 1];
-    if (!spans) {
-        std::snprintf(g_last_hip_error, sizeof g_last_hip_error, "out of host memory");
-        return BITNET_ERR_HIP;
-    }
-    size_t m = 0;
-    for (int64_t i = 0; i < count; ++i) {
-        if (n[i] == 0) continue;
-        const uintptr_t bytes = (uintptr_t)n[i] * (dtype[i] == BITNET_OUT_F32 ? 4 : 2);
-        const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(out[i]);
-        spans[m++] = {o, o + bytes, true};
-        if (g != o) spans[m++] = {g, g + bytes, false};
-    }
-    std::sort(spans, spans + m, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    constexpr int kSpans = 2048, kKeep = kSpans / 2;
+    Span buf[kSpans];
+    Span seen = {0, -1};
     uintptr_t any = 0, outs = 0;
-    int st = BITNET_OK;
-    for (size_t i = 0; i < m && st == BITNET_OK; ++i) {
-        if (spans[i].begin < (spans[i].out ? any : outs)) st = BITNET_ERR_INVALID_ARG;
-        any = std::max(any, spans[i].end);
-        if (spans[i].out) outs = std::max(outs, spans[i].end);
+    bool more = true;
+    while (more) {
+        more = false;
+        int m = 0;
+        Span most = {UINTPTR_MAX, INT64_MAX};
+        for (int64_t t = 0; t < count; ++t) {
+            if (n[t] == 0) continue;
+            for (int64_t i = 2 * t; i < 2 * t + (grads[t] == out[t] ? 1 : 2); ++i) {
+                const Span s = {reinterpret_cast<uintptr_t>(i & 1 ? grads[t] : out[t]), i};
+                if (!(seen < s) || !(s < most)) continue;
+                if (m == kSpans) {
+                    std::nth_element(buf, buf + kKeep, buf + m);
+                    m = kKeep;
+                    most = buf[kKeep];
+                    more = true;
+                    if (!(s < most)) continue;
+                }
+                buf[m++] = s;
+            }
+        }
+        std::sort(buf, buf + m, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+        for (int k = 0; k < m; ++k) {
+            const int64_t t = buf[k].i >> 1;
+            const bool is_out = (buf[k].i & 1) == 0;
+            if (buf[k].begin < (is_out ? any : outs)) return BITNET_ERR_INVALID_ARG;
+            const uintptr_t end = buf[k].begin + (uintptr_t)n[t] * (dtype[t] == BITNET_OUT_F32 ? 4 : 2);
+            any = std::max(any, end);
+            if (is_out) outs = std::max(outs, end);
+        }
+        if (more) seen = *std::max_element(buf, buf + m);
     }
-    delete[] spans;
-    return st;
+    return BITNET_OK;
 }
 
 int bitnet_clip_grads(int64_t count, const void* const* grads, void* const* out, const int64_t* n,

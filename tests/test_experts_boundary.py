@@ -2,6 +2,7 @@
 arguments are refused on the host before any HIP call, empty problems are accepted, and the
 Python binding refuses CPU tensors."""
 import ctypes
+import subprocess
 
 import pytest
 import torch
@@ -135,6 +136,50 @@ def test_overlaps_are_found_by_the_sorted_spans(L):
             st = L.bitnet_clip_grads(6, ptrs(*g), ptrs(*o), i64s(*n), i32s(*[0] * 6), 1.0, None, A, B, ws, None)
             assert st in (HIP, DEVICE), (n, g, o)
     assert seen == {False, True}
+
+
+@pytest.mark.parametrize("count", [255, 256, 257, 600, 3000])
+def test_overlaps_in_long_lists(L, count):
+    # spans side by side in any order, in place or not; then one of them reaches over another's first value
+    import random
+    rng = random.Random(count)
+    places = list(range(2 * count))
+    rng.shuffle(places)
+    ws = L.bitnet_grad_norm_workspace_size(count)
+    n = [rng.randint(1, 16) for _ in range(count)]
+    g = [0x100000 + 64 * places[2 * i] for i in range(count)]
+    o = [p if rng.random() < 0.5 else 0x100000 + 64 * places[2 * i + 1] for i, p in enumerate(g)]
+
+    def f(g, o, n):
+        return L.bitnet_clip_grads(count, ptrs(*g), ptrs(*o), i64s(*n), i32s(*[0] * count), 1.0, None, A, B, ws, None)
+    if not torch.cuda.is_available():  # (a call that passes would reach the device)
+        assert f(g, o, n) in (HIP, DEVICE)
+    at = {p: i for i, p in enumerate(o)}
+    tried = 0
+    for i in rng.sample(range(count), min(count, 40)):
+        j = at.get(o[i] + 64)  # the output in the next place
+        if j is None:
+            continue
+        tried += 1
+        longer = list(n)
+        longer[i] = 17
+        assert f(g, o, longer) == INVALID, (i, j)
+        # the same reach from an input over that output is an overlap too, unless the output lies elsewhere
+        if g[i] != o[i] and g[j] != o[j]:
+            moved = list(o)
+            moved[i] = 0x100000 + 64 * (2 * count + 5)
+            assert f(g[:i] + [o[i]] + g[i + 1:], moved, longer) == INVALID, (i, j)
+            if not torch.cuda.is_available():
+                free = list(o)
+                free[i], free[j] = 0x100000 + 64 * (2 * count + 5), 0x100000 + 64 * (2 * count + 9)
+                assert f(g[:i] + [o[i]] + g[i + 1:], free, longer) in (HIP, DEVICE), (i, j)
+    assert tried > 0
+
+
+def test_the_library_allocates_nothing_on_the_host(L):
+    names = subprocess.run(["nm", "-D", "--undefined-only", bw.library_path()], capture_output=True, text=True,
+                           check=True).stdout.split()
+    assert not [n for n in names if n.startswith(("_Znw", "_Zna", "malloc", "calloc", "realloc", "aligned_alloc"))]
 
 
 def test_expert_order_validation(L):
