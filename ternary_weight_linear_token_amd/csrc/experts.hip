@@ -184,10 +184,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
         voff_b[i] = row < rows_b ? (uint32_t)(row * row_bytes) + skew + 16 * q : kOut;
     }
 
-    // Activations are loaded D steps before they go to LDS, weights DB - 1 steps before their use.
-    constexpr int DB = D > 2 ? D : 2;
-    static_assert(D == 1 || D == 2 || D == 4, "sets go round with the stages");
-    u32x4 ar[D][NA], br[DB][NB];
+    // Activations are loaded D steps before they go to LDS, weights one step before their use.
+    static_assert(D == 1 || D == 2, "sets go round with the stages");
+    u32x4 ar[D][NA], br[2][NB];
     auto load_a = [&](int set, int j, int step) {
         const int k0 = (step * G + g) * BK;
         // a chunk behind the row's end reads zeros; soff 0 keeps kOut from wrapping
@@ -261,9 +260,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[j][i][r] = 0;
 
-    // Step it multiplies stage it % 2 and weight set it % DB, while the activations of step it + 1, in
+    // Step it multiplies stage and weight set it % 2, while the activations of step it + 1, in
     // registers, go into the other stage and their registers are loaded for step it + 1 + D, and
-    // the weight set of step it - 1 for it + DB - 1.  One barrier a step, before its last 32 k, whose
+    // the other weight set for step it + 1.  One barrier a step, before its last 32 k, whose
     // operands are already in registers; the first operands of the next step are read behind it.
     constexpr int NM = MB * NB, S = (KS - 1) * NM;  // slots; those before the barrier
 #pragma unroll
@@ -272,10 +271,6 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
     for (int d = 0; d < D; ++d)
 #pragma unroll
         for (int j = 0; j < NA; ++j) load_a(d, j, d);
-#pragma unroll
-    for (int d = 1; d < DB - 1; ++d)
-#pragma unroll
-        for (int i = 0; i < NB; ++i) load_b(d, i, d);
 #pragma unroll
     for (int j = 0; j < NA; ++j) {
         mask_a(0, j, 0);
@@ -288,10 +283,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
 #pragma unroll
     for (int e = 0; e < 4 * NB; ++e) expand(op[0], br[0], 0, e);
     auto step = [&](int it, auto at_c) {
-        constexpr int at = decltype(at_c)::value;  // it modulo the sets
-        constexpr int a_set = (at + 1) % D, b_set = at % DB, b_next = (at + 1) % DB, b_load = (at + DB - 1) % DB;
-        const uint8_t* const cur = lds + (at & 1) * kStage;
-        uint8_t* const nxt = lds + ((at & 1) ^ 1) * kStage;
+        constexpr int at = decltype(at_c)::value;  // it % 2
+        constexpr int a_set = (at + 1) % D;
+        const uint8_t* const cur = lds + at * kStage;
+        uint8_t* const nxt = lds + (at ^ 1) * kStage;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const bool last = s == KS - 1;
@@ -303,14 +298,14 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
                 acc[m % MB][m / MB] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[m / MB], o.x[m % MB],
                                                                             acc[m % MB][m / MB], 0, 0, 0);
                 const int slot = s * NM + m;
-                if (slot < NB) load_b(b_load, slot, it + DB - 1);
+                if (slot < NB) load_b(at ^ 1, slot, it + 1);
 #pragma unroll
                 for (int j = 0; j < MB; ++j)
                     if (j * ((NM + 1) / 2) / MB == m) read(n, last ? nxt : cur, last ? 0 : s + 1, j);
 #pragma unroll
                 for (int e = 0; e < 4 * NB; ++e)
                     if (NM / 2 + e * (NM - NM / 2) / (4 * NB) == m)
-                        expand(n, br[last ? b_next : b_set], last ? 0 : s + 1, e);
+                        expand(n, br[last ? at ^ 1 : at], last ? 0 : s + 1, e);
 #pragma unroll
                 for (int j = 0; j < NA; ++j)
                     if (j * S / NA + S / NA / 2 == slot) {
@@ -322,22 +317,14 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN) * G, W) void expert_tile
             }
         }
     };
-    // whole rounds of the sets, then what is left (an exit inside the loop would give the
-    // accumulators a second live range)
+    // pairs of steps, then the odd one (an exit inside the loop would give the accumulators a
+    // second live range)
     int it = 0;
-    for (; it + DB <= nsteps; it += DB) {
+    for (; it + 2 <= nsteps; it += 2) {
         step(it, std::integral_constant<int, 0>());
         step(it + 1, std::integral_constant<int, 1>());
-        if constexpr (DB > 2) {
-            step(it + 2, std::integral_constant<int, 2>());
-            step(it + 3, std::integral_constant<int, 3>());
-        }
     }
     if (it < nsteps) step(it, std::integral_constant<int, 0>());
-    if constexpr (DB > 2) {
-        if (it + 1 < nsteps) step(it + 1, std::integral_constant<int, 1>());
-        if (it + 2 < nsteps) step(it + 2, std::integral_constant<int, 2>());
-    }
 
     // ---- outputs: lane (l32, q) of block (j, i) has row 32 j + l32, columns 32 i + 8 c + 4 q + 0 .. 3 in
     // registers 4 c ..; eight registers at a time (h: c = 2 h and 2 h + 1) ----
@@ -601,7 +588,7 @@ hipError_t launch_units(KERNEL kernel, ExpertArgs a, int bm, int bn, int threads
     a.tiles_n = (int)tn;
     a.panel = panel;
     const int64_t units = expert_tiles(a.P, a.E, bm) * tn;
-    // (units of 16 x 16 outputs at least: more than the card holds)
+    // (at most 2^15 column tiles, of four matrices of 2^20 rows: more outputs than the card holds)
     if (units > INT32_MAX) return hipErrorInvalidValue;
     const int64_t most = max_blocks(threads) / kXcds * kXcds;
     const int64_t blocks = (units + kXcds - 1) / kXcds * kXcds;
