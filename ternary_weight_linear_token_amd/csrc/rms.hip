@@ -457,14 +457,19 @@ hipError_t launch_rms_back_v(const RmsBackArgs& a, hipStream_t stream) {
         case 4: hipLaunchKernelGGL((rmsnorm_back_kernel<V, 4, 1, CODES, RES>), grid, dim3(512), 0, stream, a); break;
         case 8: hipLaunchKernelGGL((rmsnorm_back_kernel<V, 8, 1, CODES, RES>), grid, dim3(512), 0, stream, a); break;
         case 16:
-            // two groups a lane with 16 waves fill a CU with one block; eight waves with three leave
-            // room for two (8191 x 4100 from a checkpoint: 57 -> 40 us)
-            if (V == 4 && a.K > (int64_t)16 * 64 * V && a.K <= (int64_t)8 * 64 * 3 * V)
-                hipLaunchKernelGGL((rmsnorm_back_kernel<V, 8, 3, CODES, RES>), grid, dim3(512), 0, stream, a);
-            else if (a.K <= (int64_t)16 * 64 * V)
+            if (a.K <= (int64_t)16 * 64 * V) {
                 hipLaunchKernelGGL((rmsnorm_back_kernel<V, 16, 1, CODES, RES>), grid, dim3(1024), 0, stream, a);
-            else
-                hipLaunchKernelGGL((rmsnorm_back_kernel<V, 16, 2, CODES, RES>), grid, dim3(1024), 0, stream, a);
+                break;
+            }
+            // two groups a lane with 16 waves fill a CU with one block; eight waves with three leave
+            // room for two (8191 x 4100 from a checkpoint: 57 -> 40 us; rows of whole eights never come
+            // here with three)
+            if constexpr (V == 4)
+                if (a.K <= (int64_t)8 * 64 * 3 * V) {
+                    hipLaunchKernelGGL((rmsnorm_back_kernel<V, 8, 3, CODES, RES>), grid, dim3(512), 0, stream, a);
+                    break;
+                }
+            hipLaunchKernelGGL((rmsnorm_back_kernel<V, 16, 2, CODES, RES>), grid, dim3(1024), 0, stream, a);
             break;
         default: {
             const unsigned rows = (unsigned)(a.M < 1024 ? a.M : 1024);
