@@ -3,8 +3,8 @@ import pytest
 import torch
 
 import ternary_weight_linear_token_amd as bw
-from test_gpu_experts import experts, offsets_of
-from test_gpu_train import bf16
+from test_gpu_experts import experts, offsets_of, spread
+from test_gpu_train import bf16, check_grad_input
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,28 @@ def test_product_of_more_tiles_than_a_launch():
                 n = min(4093 << 12, at + c - lo)
                 assert torch.equal(outs[g][lo:lo + n], want.roll(-(lo % 4093), 0).repeat(n // 4093 + 1, 1)[:n])
             at += c
+
+
+# input gradients of several stacks that go from one to the next in each kernel: sums of several
+# steps, with stacks of a part of a step and of nothing between them
+SEVERAL = [(1500, 64, (200, 72), 2064), (1500, 64, (201, 77), 2052), (1500, 64, (75, 3, 0, 201), 1540),
+           (300, 16, (200, 136), 2560), (300, 16, (201, 3, 77, 130), 2564), (100, 4, (200, 8, 0, 136), 2064),
+           (100, 4, (201, 77), 2052), (100, 4, (640, 712), 2064), (100, 4, (641, 5, 0, 713), 2052)]
+
+
+@pytest.mark.parametrize("P,E,Ns,K", SEVERAL)
+@pytest.mark.parametrize("kind", ["even", "skewed"])
+def test_input_gradient_across_stacks(P, E, Ns, K, kind):
+    counts = spread(P, E, 3, kind)
+    off = offsets_of(counts)
+    dys = [bf16(P, n, seed=n + i, scale=1e-3, hot=False) for i, n in enumerate(Ns)]
+    w = [experts(E, n, K, seed=n + i) if n else (torch.empty((E, 0, K // 4), dtype=torch.uint8, device="cuda"),
+                                                 torch.empty((E, 0), device="cuda")) for i, n in enumerate(Ns)]
+    got = bw.grad_input_experts_grouped(dys, off, [p for p, _ in w], [s for _, s in w])
+    at = 0
+    for e, c in enumerate(counts):
+        if c:
+            check_grad_input([d[at:at + c] for d, n in zip(dys, Ns) if n],
+                             [p[e].clone() for (p, _), n in zip(w, Ns) if n],
+                             [s[e].clone() for (_, s), n in zip(w, Ns) if n], K, got[at:at + c], f"{kind} expert {e}")
+        at += c
