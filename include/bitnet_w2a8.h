@@ -632,7 +632,9 @@ int bitnet_gemm_experts(const int8_t* xq, const float* a_scale, int64_t T, const
  * bitnet_grad_input_experts -- bitnet_grad_input of every expert's rows (without workspace):
  *   dx[p,k] = sum_g sum_n dy_g[p,n] * w_scale_g[e,n] * w_g[e,n,k], bf16 (P, K), in the rows' order
  *   (bitnet_combine_experts adds up the rows of a token).
- *   dy : HOST array of bf16 (P, N[g]) device pointers; packed, w_scale, N as above.
+ *   dy : HOST array of bf16 (P, N[g]) device pointers; packed, w_scale, N as above.  As in
+ *        bitnet_grad_input each dy * w_scale is rounded to bf16 once (2^-8 of itself at most), and an
+ *        unused code 0b11 counts as weight 0.
  */
 int bitnet_grad_input_experts(const int32_t* offsets, int64_t P, int64_t E, int64_t K, int64_t groups,
                               const uint16_t* const* dy, const uint8_t* const* packed,
@@ -642,7 +644,9 @@ int bitnet_grad_input_experts(const int32_t* offsets, int64_t P, int64_t E, int6
 /*
  * bitnet_grad_weight_experts -- bitnet_grad_weight of every expert's rows (without splitting):
  *   dw[e,n,k] = sum over the rows p of e of dy[p,n] * xq[t,k] / a_scale[t],  t = rows[p] (or p).
- *   dy        : bf16 (P, N).   xq, a_scale, T, rows, offsets : as in bitnet_gemm_experts.
+ *   dy        : bf16 (P, N).   xq, a_scale, T, rows, offsets : as in bitnet_gemm_experts.  As in
+ *               bitnet_grad_weight each xq * (1 / a) is rounded to bf16 once: not at all for
+ *               power-of-two scales (BITNET_SCALE_POW2), by up to 2^-8 of itself for absmax ones.
  *   dw        : (E, N, K), BITNET_OUT_F32 or BITNET_OUT_BF16; zeros for an expert without rows.
  *   workspace : with rows, bitnet_grad_weight_experts_workspace_size(P, K) bytes (the codes in the
  *               rows' order; else BITNET_ERR_WORKSPACE); calls that share one must be ordered.

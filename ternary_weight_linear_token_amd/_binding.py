@@ -1063,7 +1063,8 @@ def grad_input_experts_grouped(dy, offsets, packed, w_scale, out=None):
     """Gradient of gemm_experts_grouped with respect to its activations, bf16 (P, K) in the rows'
     order (combine_experts(dx, slots) adds up the rows of a token).
 
-    dy: sequence of bf16 (P, N_g).  Rows behind offsets[-1] are not written."""
+    dy: sequence of bf16 (P, N_g).  Rows behind offsets[-1] are not written.  Each dy * w_scale is
+    rounded to bf16 once before its products."""
     if len(dy) == 0 or len(dy) != len(packed):
         raise ValueError("dy, packed and w_scale must have the same length, at least 1")
     P = _rows(dy[0], "dy[0]")[0]
@@ -1089,8 +1090,9 @@ def grad_input_experts(dy, offsets, packed, w_scale, out=None):
 def grad_weight_experts(dy, xq, a_scale, offsets, out_dtype="f32", rows=None, out=None,
                         workspace=None):
     """Gradient of gemm_experts with respect to the latent weights, (E, N, K): for every expert
-    dy^T (xq / a_scale) over its rows; zeros for an expert without rows.  dy: bf16 (P, N); xq,
-    a_scale, rows: as in gemm_experts_grouped.  workspace: with rows, uint8 scratch of
+    dy^T (xq / a_scale) over its rows; zeros for an expert without rows.  xq / a_scale is rounded to
+    bf16 once: exact for codes with power-of-two scales (scale="pow2"), not for absmax codes.  dy: bf16
+    (P, N); xq, a_scale, rows: as in gemm_experts_grouped.  workspace: with rows, uint8 scratch of
     bitnet_grad_weight_experts_workspace_size bytes (allocated by default)."""
     P, N = _rows(dy, "dy")
     T, K = _rows(xq, "xq")

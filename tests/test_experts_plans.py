@@ -8,7 +8,7 @@ import pytest
 
 from ternary_weight_linear_token_amd import build as bw_build
 from test_gpu_experts import GRADS, test_large_gradients as large
-from test_gpu_experts_limits import SEVERAL
+from test_gpu_experts_limits import SEVERAL, test_weight_gradient_against_the_codes_values as operands
 
 LARGE_GRADS = next(m.args[1] for m in large.pytestmark if m.args[:1] == ("P,E,N,K",))
 
@@ -97,6 +97,13 @@ def test_gpu_sizes_reach_every_kernel(taken):
     one = {taken(0, P, E, K, [N]) for P, E, N, K in GRADS + LARGE_GRADS}
     one |= {taken(w, P, E, K, [N]) for P, E, N, K in GRADS + LARGE_GRADS for w in (1, 2)}
     assert one == want
+
+
+def test_gpu_sizes_check_the_weight_gradients_operands_in_every_kernel(taken):
+    want, cfgs = compiled()
+    sizes = next(m.args[1] for m in operands.pytestmark if m.args[:1] == ("P,E,N,K",))
+    for w in (1, 2):
+        assert {taken(w, P, E, K, [N]) for P, E, N, K in sizes} == {(c, r) for c, r in want if cfgs[c][0]}
 
 
 def test_gpu_sizes_cross_between_stacks_in_every_kernel(taken):

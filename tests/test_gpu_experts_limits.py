@@ -4,7 +4,7 @@ import torch
 
 import ternary_weight_linear_token_amd as bw
 from test_gpu_experts import experts, offsets_of, spread
-from test_gpu_train import bf16, check_grad_input
+from test_gpu_train import BF, TINY, U, bf16, check_grad_input, close
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,40 @@ def test_input_gradient_across_stacks(P, E, Ns, K, kind):
                              [p[e].clone() for (p, _), n in zip(w, Ns) if n],
                              [s[e].clone() for (_, s), n in zip(w, Ns) if n], K, got[at:at + c], f"{kind} expert {e}")
         at += c
+
+
+# one size for each kernel of the weight gradient
+@pytest.mark.parametrize("P,E,N,K", [(700, 8, 300, 516), (300, 3, 257, 1028), (1200, 2, 256, 256), (4100, 4, 33, 64),
+                                     (1700, 4, 1280, 4100), (1100, 3, 1281, 1028)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", ["absmax", "pow2"])
+def test_weight_gradient_against_the_codes_values(P, E, N, K, dt, scale):
+    # against sum dy xq / a itself.  Of absmax codes each xq / a takes the reciprocal (1 ulp and a Newton
+    # step: one rounding), a product and the rounding to bf16; of powers of two none of them rounds
+    counts = spread(P, E, P, "skewed")
+    dy = bf16(P, N, seed=N, scale=1e-3, hot=False)
+    xq, a = (bw.quant_act if scale == "absmax" else bw.quant_act_pow2)(bf16(P, K, seed=K))
+    out = bw.grad_weight_experts(dy, xq, a, offsets_of(counts), dt)
+    operand = BF * (1 + 3 * U) + 3 * U if scale == "absmax" else 0.0
+    at = 0
+    for e, c in enumerate(counts):
+        if c:
+            d = dy[at:at + c].double().t().contiguous()
+            x = xq[at:at + c].double() / a[at:at + c].double()[:, None]
+            ref, size = d @ x, d.abs() @ x.abs()
+            tol = (operand + (c + 64) * U * (1 + operand)) * size + TINY
+            if dt == "bf16":
+                tol = (1 + BF) * tol + BF * ref.abs()
+            close(out[e], ref, tol, f"expert {e}")
+        at += c
+
+
+@pytest.mark.parametrize("P,E,N,K", [(20, 3, 32, 64), (20, 3, 33, 68), (1500, 64, 40, 2064)])
+def test_input_gradient_unused_code_is_zero(P, E, N, K):
+    counts = spread(P, E, 1, "even")
+    packed, s = experts(E, N, K, seed=1)
+    dy = bf16(P, N, seed=1, hot=False)
+    unused, zero = packed.clone(), packed.clone()
+    unused[:, 7], zero[:, 7] = 0xFF, 0x55
+    a, b = (bw.grad_input_experts(dy, offsets_of(counts), p, s) for p in (unused, zero))
+    assert torch.equal(a, b)
