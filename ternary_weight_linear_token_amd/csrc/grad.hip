@@ -849,7 +849,8 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
 }
 
 // ---- grouped by expert ----
-// Tiles of the experts' gradients (mode, bm, bn, wm, wn, g, bl, d, w); none is split over blocks.
+// Tiles of the experts' gradients (mode, bm, bn, wm, wn, g, bl, d, w); none is split over blocks.  "r of E":
+// r rows of each of E experts.
 // dw: 128 x 128, three blocks on a CU (fp32, 216 rows of 37, 384 x 2752: 50 us; two blocks and steps of 64
 // rows 57; 3 of 44, 320 x 2992: 27 us, 256 x 128 30; bf16, 23 of 38, 6733 x 516: 99 us, four blocks 111).
 // Hundreds of rows or thousands of tiles: 256 x 128 (bf16, 1393 of 7, 2112 x 2496: 143 us against 150; 124
@@ -861,15 +862,18 @@ hipError_t launch_grad(int mode, GradArgs a, const int64_t* L, bool aligned, voi
 // 1024: 27 us against 34; N odd, 2228 of 6, 343 x 640: 39 with two steps in flight, 45 with one).
 // dx, by the number of 32 x 128 tiles: from 800 on 64 x 256, whose rows are padded little and converted
 // for 256 columns at once (512 rows of 8, 6912 x 2560: 158 us; 64 x 128 190, 128 x 128 185, 256 x 256 190;
-// with 840 tiles 19 against 27, with 504 67 against 53).  Rows off 16 bytes take two loads a chunk, which
-// want two steps in flight; two blocks share a CU then, not three, so that is for tiles that fill
-// one round of two or two of them (258 rows of 4, 5471 x 6316, 500 tiles of 64 x 256: 135 us against 186;
-// 191 of 8, 895 x 11672, 828: 52 against 67; but 539 of 4, 3319 x 3652, 540: 152 against 119).  Below 800
-// tiles 32 x 128 with four groups of waves (258 rows of 16, 641 x 2564: 14 us against 24; 64 of 8, 6912 x
-// 2560: 46 against 72), at no more than one for each CU with two steps in flight, for which there are
-// registers then (58 rows of 6, 4653 x 1176: 36 us against 45; of one step 512 x 1176 and below the same;
-// with 266 tiles 16 against 12).  Long sums in half as many: 32 x 64 with eight groups, half the steps (2
-// rows of 3, 13666 x 1664: 53 us against 87; 10 of 10, 5311 x 1296: 29 against 39; with 150 31 against 22).
+// 96 of 14, 640 x 2560, 840 tiles: 15 against 18 in 32 x 128; 60 of 14, 6912 x 2560, 560: 76 against 62).
+// Rows off 16 bytes take two loads a chunk, which want two steps in flight; two blocks share a CU then,
+// not three, so that is for tiles that fill one round of two or two of them (258 of 4, 5471 x 6316: 128 us
+// against 180; 342 of 5, 3429 x 3592: 79 against 114; but 539 of 4, 3319 x 3652: 146 against 114).  Their
+// number is taken with half a tile of padding for an expert: rows that need less may get the wrong one
+// (191 of 5, 895 x 11672, 690 tiles for 828: 45 against 37).  Below 800 tiles 32 x 128 with four groups
+// of waves (16 of 16, 641 x 2564, 336 tiles: 13 us against 20; 64 of 8, 6912 x 2560, 320: 41 against 67),
+// at no more than one for each CU with two steps in flight, for which there are registers then (30 of
+// 10, 5311 x 1920, 150 tiles: 38 us against 49; 8 of 8, 6912 x 2560, 160: 25.6 against 26.7; 58 of 6, 640 x
+// 1176 the same 9; with 260, 8 of 13, 2560 x 2560, 24 against 19).  Long sums in half as many: 32 x 64 with
+// eight groups, half the steps (58 of 6, 4653 x 1176, 120 tiles: 25 us against 33; 2 of 3, 13666 x 1664:
+// 50 against 82; 10 of 10, 5311 x 1296: 27 against 36; with 150, 30 of 10, 5311 x 1920, 54 against 38).
 constexpr GradCfg kExpertCfg[] = {
     {0, 256, 128, 128, 64, 1, 32, 1, 2, 2, 0, 0, 0},
     {0, 128, 128, 64, 64, 1, 64, 2, 2, 2, 0, 0, 0},

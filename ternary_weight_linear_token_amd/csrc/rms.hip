@@ -13,7 +13,10 @@
 // block is on its way meanwhile.  Sums are fp32 in a fixed order.
 // Measured: 2048 x 4096 with residual, codes and statistics 11.2 us (58.7 MB, 5.2 TB/s of which part
 // stays in a cache); 1 x 2560 2.6 us; backward 8191 x 4100 from a checkpoint 38 to 41 us (235 MB, 5.9
-// TB/s) and 4.7 for the join of the 512 partial column sums.
+// TB/s) and 4.7 for the join of the 512 partial column sums.  From bf16 with the residual's gradient, join
+// included, replayed: 4096 x 8192 57 us (4.7 TB/s); 2048 x 12288 54 (3.7; from a checkpoint 53, 3.3), where a
+// lane keeps 8 (16) of its values in scratch; 2048 x 16388, whose rows no block holds and which are read
+// three times, 110 (2.4).
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "rows.hpp"

@@ -1,5 +1,5 @@
-// rows.hpp -- helpers of the kernels that work on whole rows (quantization, layer norm, SwiGLU): groups
-// of V bf16 elements, reductions over the waves of one row, int8 codes and their scales.
+// rows.hpp -- helpers of the kernels that work on whole rows (quantization, the norms, SwiGLU, sums of
+// experts' rows): groups of V bf16 elements, reductions over the waves of one row, int8 codes and their scales.
 #pragma once
 
 #include <type_traits>
